@@ -9,4 +9,6 @@ from .fp4 import (  # noqa: F401
     fp4_status_string, fp4_packed_bytes, fp4_scale_bytes, fp4_compute_global_scale,
     fp4_quantize, fp4_alpha_from_global_scales, fp4_gemm, fp4_gemm_workspace_bytes,
     fp4_get_device_status, quantize, global_scale, gemm, lib,
+    BF16, FP16, fp4_quantize_int8, fp4_gemm_int8, fp4_gemm_int8_grouped, quantize_int8, gemm_int8,
+    gemm_int8_grouped, linear_int8,
 )

@@ -16,7 +16,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp4.so")
-SOURCES = ["api.cu", "quantize.cu", "gemm.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "quantize_int8.cu", "gemm_int8.cu"]
 HEADERS = ["fp4_internal.h", "quant_device.cuh", "tc_device.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 

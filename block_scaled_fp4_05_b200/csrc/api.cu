@@ -67,6 +67,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Formats of the GEMM and quantizer entry points.
 bool valid_fmt(fp4_format f) { return f == FP4_NVFP4 || f == FP4_MXFP4 || f == FP4_P1E8; }
 bool valid_quant_fmt(fp4_format f) { return valid_fmt(f); }
+bool valid_dtype(fp4_dtype t) { return t == FP4_BF16 || t == FP4_FP16; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 fp4_status from_cuda(cudaError_t e)
 {
@@ -92,6 +94,11 @@ constexpr int64_t kMaxRows = (int64_t)1 << 31;
 // Rowwise tiles (128 rows x 4 blocks) of one tensor: a batched launch puts
 // the tiles of up to 8 tensors in one 1-D grid.
 constexpr int64_t kMaxRowTiles = (int64_t)1 << 28;
+// INT8 products: exact 32-bit sums for any codes, tile counts in 32 bits,
+// strides a tensor map can hold.
+constexpr int64_t kInt8MaxK = 131071;
+constexpr int64_t kMaxInt8Tiles = (int64_t)1 << 26;   // of 256 x 128; D has terabytes there
+constexpr int64_t kMaxMapStride = (int64_t)1 << 40;
 
 }  // namespace
 
@@ -560,6 +567,102 @@ fp4_status fp4_gemm_decode_noalloc(fp4_format fmt, const void* A, const void* sA
                                 fp4::noalloc_scratch_bytes(), FP4_GEMM_DECODE, stream);
 }
 
+fp4_status fp4_quantize_int8(const void* in, fp4_dtype in_dtype, int64_t rows_in, int64_t cols, int64_t ld,
+                             const int32_t* row_index, int64_t rows, void* codes_out, int64_t ld_codes,
+                             float* scales_out, fp4_stream_t stream)
+{
+    fp4::g_last_error[0] = 0;
+    if (!valid_dtype(in_dtype) || rows_in < 0 || cols < 0 || rows < 0 || ld < cols || ld_codes < cols)
+        return FP4_ERR_INVALID_ARG;
+    if (!row_index && rows != rows_in) return FP4_ERR_INVALID_ARG;
+    if (rows == 0) return FP4_OK;
+    if (!scales_out || (cols > 0 && (!codes_out || (rows_in > 0 && !in)))) return FP4_ERR_INVALID_ARG;
+    if (rows >= kMaxRows || rows_in >= kMaxRows || cols >= kMaxRows) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (ld % 8 != 0 || ld_codes % 16 != 0 || !aligned16(in) || !aligned16(codes_out) || !aligned4(scales_out) ||
+        !aligned4(row_index))
+        return FP4_ERR_MISALIGNED;
+    fp4::DeviceInfo dev;
+    fp4_status st = require_device(&dev);
+    if (st != FP4_OK) return st;
+    return from_cuda(fp4::launch_quantize_int8((int)in_dtype, static_cast<const uint16_t*>(in), rows_in, cols, ld,
+                                               row_index, rows, static_cast<int8_t*>(codes_out), ld_codes,
+                                               scales_out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Shared part of the two INT8 products: M rows of A and D (all experts'
+// together in the grouped form).
+static fp4_status gemm_int8(const void* A, int64_t lda, const float* sA, const void* B, int64_t ldb,
+                            int64_t stride_b, const float* sB, const int32_t* offsets, int64_t E, int64_t M,
+                            int64_t N, int64_t K, const float* bias, fp4_dtype out_dtype, void* D, int64_t ldd,
+                            fp4_gemm_kernel kernel, fp4_stream_t stream)
+{
+    const int flags = (int)kernel & ~0xFF;
+    const int choice = (int)kernel & 0xFF;
+    if (choice != FP4_GEMM_AUTO && choice != FP4_GEMM_PREFILL && choice != FP4_GEMM_DECODE)
+        return FP4_ERR_INVALID_ARG;
+    if (flags & ~(int)FP4_GEMM_B_STATIC) return FP4_ERR_INVALID_ARG;
+    if (!valid_dtype(out_dtype) || M < 0 || N < 0 || K < 0 || lda < K || ldb < K || ldd < N)
+        return FP4_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || E == 0) return FP4_OK;
+    if (!D || !sA || !sB) return FP4_ERR_INVALID_ARG;
+    if (K > 0 && (!A || !B)) return FP4_ERR_INVALID_ARG;
+    // K: 128 * 128 * K stays below 2^31.  M, N: tile counts in 32 bits.
+    if (K > kInt8MaxK || M >= kMaxRows || N >= kMaxRows) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if ((M / 256 + E) * ((N + 127) / 128) > kMaxInt8Tiles) return FP4_ERR_UNSUPPORTED_SHAPE;
+    // tensor-map strides are below 2^40 bytes
+    if (lda >= kMaxMapStride || ldb >= kMaxMapStride || stride_b >= kMaxMapStride || ldd >= kMaxMapStride / 2)
+        return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (E == 1) stride_b = ldb;   // not used
+    else if (stride_b < (N - 1) * ldb + K) return FP4_ERR_INVALID_ARG;   // experts would overlap
+    if (lda % 16 != 0 || ldb % 16 != 0 || stride_b % 16 != 0 || ldd % 8 != 0 || !aligned16(A) || !aligned16(B) ||
+        !aligned16(D) || !aligned4(sA) || !aligned4(sB) || !aligned4(bias) || !aligned4(offsets))
+        return FP4_ERR_MISALIGNED;
+    fp4::DeviceInfo dev;
+    fp4_status st = require_device(&dev);
+    if (st != FP4_OK) return st;
+    if (!fp4::tensor_map_encoder_available()) return FP4_ERR_NO_DEVICE;
+    fp4::Int8GemmArgs a;
+    a.A = static_cast<const int8_t*>(A);
+    a.lda = lda;
+    a.sA = sA;
+    a.B = static_cast<const int8_t*>(B);
+    a.ldb = ldb;
+    a.stride_b = stride_b;
+    a.sB = sB;
+    a.offsets = offsets;
+    a.E = E;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.bias = bias;
+    a.half_out = out_dtype == FP4_FP16;
+    a.D = static_cast<uint16_t*>(D);
+    a.ldd = ldd;
+    a.b_static = (flags & FP4_GEMM_B_STATIC) != 0;
+    return from_cuda(fp4::launch_gemm_int8(a, choice, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_gemm_int8(const void* A, int64_t lda, const float* sA, const void* B, int64_t ldb,
+                         const float* sB, int64_t M, int64_t N, int64_t K, const float* bias,
+                         fp4_dtype out_dtype, void* D, int64_t ldd, fp4_gemm_kernel kernel, fp4_stream_t stream)
+{
+    fp4::g_last_error[0] = 0;
+    return gemm_int8(A, lda, sA, B, ldb, ldb, sB, nullptr, 1, M, N, K, bias, out_dtype, D, ldd, kernel, stream);
+}
+
+fp4_status fp4_gemm_int8_grouped(const void* A, int64_t lda, const float* sA, const void* B, int64_t ldb,
+                                 int64_t stride_b, const float* sB, const int32_t* offsets, int64_t E,
+                                 int64_t T, int64_t N, int64_t K, const float* bias, fp4_dtype out_dtype,
+                                 void* D, int64_t ldd, fp4_gemm_kernel kernel, fp4_stream_t stream)
+{
+    fp4::g_last_error[0] = 0;
+    if (E < 0 || stride_b < 0) return FP4_ERR_INVALID_ARG;
+    if (E > fp4::kInt8MaxExperts) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (E > 0 && T > 0 && N > 0 && !offsets) return FP4_ERR_INVALID_ARG;
+    return gemm_int8(A, lda, sA, B, ldb, stride_b, sB, offsets, E, T, N, K, bias, out_dtype, D, ldd, kernel,
+                     stream);
+}
+
 fp4_status fp4_selftest_bounded_wait(fp4_stream_t stream)
 {
     fp4::g_last_error[0] = 0;
@@ -576,6 +679,10 @@ fp4_status fp4_get_device_status(fp4_stream_t stream)
     unsigned int word = 0;
     e = fp4::read_and_clear_error_word(&word);
     if (e != cudaSuccess) return from_cuda(e);
+    unsigned int word_int8 = 0;   // the INT8 kernels' own word (the same bits)
+    e = fp4::read_and_clear_int8_error_word(&word_int8);
+    if (e != cudaSuccess) return from_cuda(e);
+    word |= word_int8;
     if (!word) return FP4_OK;
     e = fp4::clear_noalloc_counters(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return from_cuda(e);

@@ -94,6 +94,31 @@ cudaError_t current_context(void** ctx);
 constexpr unsigned int kErrorWorkspaceBit = 64u;
 int tensor_map_encoder_available();
 
+// quantize_int8.cu
+cudaError_t launch_quantize_int8(int dtype, const uint16_t* x, int64_t rows_in, int64_t cols, int64_t ld,
+                                 const int32_t* row_index, int64_t rows, int8_t* codes, int64_t ldc,
+                                 float* scales, cudaStream_t s);
+
+// gemm_int8.cu
+constexpr int kInt8MaxExperts = 512;   // the pair kernel keeps the experts' tile list in shared memory
+struct Int8GemmArgs {
+    const int8_t* A;          // [M x K], leading dimension lda
+    int64_t lda;
+    const float* sA;
+    const int8_t* B;          // [E x N x K], leading dimension ldb, experts stride_b apart
+    int64_t ldb, stride_b;
+    const float* sB;
+    const int32_t* offsets;   // device, [E + 1]; NULL: dense, E = 1
+    int64_t E, M, N, K;
+    const float* bias;
+    bool half_out;            // D is FP16 instead of BF16
+    uint16_t* D;
+    int64_t ldd;
+    bool b_static;
+};
+cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t read_and_clear_int8_error_word(unsigned int* word);
+
 // Records the detail of a failure for fp4_last_error() (thread-local).
 void set_last_error(const char* what, cudaError_t e);
 extern thread_local char g_last_error[256];

@@ -1,0 +1,1005 @@
+// INT8 matrix products with a scale for each token and each output channel,
+//   D[m, n] = round16( (sum_k qA[m, k] qB[n, k]) sA[m] sB[n] + bias[n] ),
+// dense, or grouped by expert: the rows [offsets[e], offsets[e + 1]) of A and
+// D belong to expert e's weights B[e], and the offsets are read on the device.
+// The sums are exact 32-bit integers (tcgen05.mma kind::i8; K <= 131071 keeps
+// them in range for any codes); the scales and the bias are applied in FP32
+// and the result is rounded once, to BF16 or FP16.
+//
+// Two kernels:
+//   int8_pair_kernel   many tokens: persistent CTA pairs, 256 x 256 (or
+//                      256 x 128) tiles.  Bound by the tensor pipe.
+//   int8_swap_kernel   few tokens: the weights on the 128-row MMA side, 16 to
+//                      128 tokens on the other, K split over a cluster whose
+//                      CTAs join their sums through distributed shared
+//                      memory.  Bound by HBM (the weights are read once).
+// Scales, bias and offsets are read past L1 (they may be written by the kernel
+// before, which can still be running when these kernels start).
+// Both take a grouped launch's tile list from the offsets themselves, so a
+// call needs no size from the device and can be captured in a graph.  Offsets
+// are clamped to [0, T] and made non-decreasing before use: whatever they
+// hold, no access leaves the tensors.
+//
+// K needs no padding: the tensor maps end at K, what a box reads behind it is
+// zero in shared memory, and zero codes add nothing.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+#include <cstdio>
+#include <mutex>
+
+#include "fp4_internal.h"
+#include "tc_device.cuh"
+
+namespace fp4 {
+namespace {
+
+constexpr int I8_BM = 128;          // rows of the A-side operand per CTA
+constexpr int I8_BK = 128;          // K elements (and bytes a row) per stage
+constexpr int I8_MMA_K = 32;        // K per tcgen05.mma kind::i8
+constexpr int I8_TILE = I8_BM * I8_BK;
+constexpr int kMaxExperts = kInt8MaxExperts;
+constexpr int64_t kI8GroupBytes = int64_t(32) << 20;
+
+struct I8Params {
+    const float* sa;         // [M]
+    const float* sb;         // [E x N]
+    const float* bias;       // [E x N] or NULL
+    uint16_t* D;             // [M x N], leading dimension ldd
+    int64_t ldd;
+    int32_t M, N;            // rows of A and D, output channels
+    int32_t ks_total;        // stages of a tile (0: K = 0, the sums are zero)
+    int32_t tiles_n;
+    int32_t raster_gm;       // pair kernel: M tiles per group of the tile order
+    int32_t E;               // experts (dense: 1)
+    const int32_t* offsets;  // [E + 1] (dense: NULL, one group of all M rows)
+    int32_t b_static;        // B is not written by the previous kernel
+};
+
+// ------------------------------------------------------------------------
+// PTX wrappers of this file
+// ------------------------------------------------------------------------
+// D (+)= A B^T in 32-bit integers, both operands signed 8-bit, K-major.
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::i8: signed 8-bit A and B (1 in bits 7 and
+// 10), 32-bit integer D (2 in bits 4-5), K-major operands, no saturation.
+__host__ __device__ constexpr uint32_t idesc_i8(int m, int n)
+{
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint32_t bar, uint32_t dst, int32_t x,
+                                            int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cluster, uint32_t dst,
+                                                 int32_t x, int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr)
+{
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    if constexpr (HALF) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    } else {
+        return pack_bf16x2(lo, hi);
+    }
+}
+
+// The scaled result of one sum; the token's scale first, so that the sum
+// leaves the integer range before the channel's scale and bias are applied.
+__device__ __forceinline__ float scaled(int acc, float sa, float sb, float bias)
+{
+    return __fmaf_rn(__fmul_rn(__int2float_rn(acc), sa), sb, bias);
+}
+
+// Inclusive prefix sum / maximum over the lanes of a warp.
+__device__ __forceinline__ int warp_scan_add(int v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+__device__ __forceinline__ int warp_scan_max(int v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v = max(v, o);
+    }
+    return v;
+}
+
+// Bounds of the 32 experts from e0 (one a lane), clamped to [0, M] and made
+// non-decreasing: first and end row of the lane's expert (empty past E).
+// `reached` carries the largest bound of the experts before e0, and leaves as
+// the largest up to here.
+__device__ __forceinline__ void expert_bounds(const I8Params& p, int e0, int lane, int& reached, int& first, int& end)
+{
+    const int e = e0 + lane;
+    int lo = 0, hi = 0;
+    if (e < p.E) {
+        lo = min(max(__ldcg(p.offsets + e), 0), p.M);
+        hi = min(max(__ldcg(p.offsets + e + 1), 0), p.M);
+    }
+    const int top = warp_scan_max(max(lo, hi), lane);   // the largest bound up to and with e + 1
+    int before = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+    if (lane == 0) before = 0;
+    first = max(max(before, reached), lo);
+    end = e < p.E ? max(max(first, hi), reached) : first;
+    reached = max(reached, __shfl_sync(0xFFFFFFFFu, top, 31));
+}
+
+// ------------------------------------------------------------------------
+// Few tokens: one CTA computes 128 output channels of up to NT tokens over
+// its share of K; the S CTAs of a cluster share the tile's K.
+//   warp 0     producer: weight and token tiles of each stage by TMA
+//   warp 1     tensor-memory allocation, MMA issue (128 x NT x 32)
+//   warps 2-5  move the accumulator to shared memory as [token][channel]
+// then all threads add the S CTAs' sums (integers: any order gives the same
+// result), each CTA for 128 / S channels, scale, and store 8 bytes at a time.
+// ------------------------------------------------------------------------
+constexpr int kSwapThreads = 192;
+
+template <int NT>
+struct SwapCfg {
+    // Two to three CTAs share an SM, so that one's first loads and last
+    // stores overlap another's stream: 72 to 100 KB each.
+    static constexpr int STAGES = NT == 16 ? 4 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+    static constexpr int STAGE_BYTES = I8_TILE + NT * I8_BK;
+    static constexpr int OFF_T = I8_TILE;
+    static constexpr int OFF_BARS = STAGES * STAGE_BYTES;
+    static constexpr int SMEM = OFF_BARS + 256 + 1024;
+    static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
+    static_assert(NT * I8_BM * 4 <= OFF_BARS, "the sums reuse the stages' memory");
+    static_assert((2 * STAGES + 2) * 8 + 32 <= 256, "barrier area");
+};
+
+template <int NT, bool HALF>
+__global__ void __launch_bounds__(kSwapThreads)
+int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                 const I8Params p)
+{
+    using C = SwapCfg<NT>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+    // [0,S) full, [S,2S) empty, [2S] accumulator full
+    int* shared_word = reinterpret_cast<int*>(bars + 2 * STAGES + 1);
+    // [0] tensor-memory base, [1] abort, [2..5] expert, first row, rows, tile within the expert
+    volatile int* abort_flag = shared_word + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    uint32_t split;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    const int rank = (int)cluster_rank();
+    const uint32_t smem0 = smem_u32(smem);
+    const uint32_t bar0 = smem_u32(bars);
+    auto FULL = [&](int s) { return bar0 + 8u * s; };
+    auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    const uint32_t acc_full = bar0 + 8u * (2 * STAGES);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(FULL(s), 1);
+            mbar_init(EMPTY(s), 1);
+        }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    // The tile: cluster c takes the c-th of the list (expert, channel tile,
+    // token tile), token tiles fastest, so that the CTAs that share weights
+    // run next to each other.
+    if (p.offsets) {
+        if (warp == 0) {
+            pdl_wait();
+            const int64_t c = blockIdx.x / split;
+            int64_t seen = 0;   // tiles of the experts before e0
+            int reached = 0, found = 0;
+            for (int e0 = 0; e0 < p.E && !found; e0 += 32) {
+                int first, end;
+                expert_bounds(p, e0, lane, reached, first, end);
+                const int mt = (end - first + NT - 1) / NT;
+                const int upto = warp_scan_add(mt, lane);   // token tiles up to this expert
+                const bool mine = c < seen + (int64_t)upto * p.tiles_n &&
+                                  c >= seen + (int64_t)(upto - mt) * p.tiles_n;
+                if (mine) {
+                    shared_word[2] = e0 + lane;
+                    shared_word[3] = first;
+                    shared_word[4] = end - first;
+                    shared_word[5] = (int)(c - seen - (int64_t)(upto - mt) * p.tiles_n);
+                }
+                found = __any_sync(0xFFFFFFFFu, mine);
+                seen += (int64_t)__shfl_sync(0xFFFFFFFFu, upto, 31) * p.tiles_n;
+            }
+            if (!found && lane == 0) shared_word[2] = -1;
+        }
+    } else if (threadIdx.x == 0) {
+        shared_word[2] = 0;
+        shared_word[3] = 0;
+        shared_word[4] = p.M;
+        shared_word[5] = (int)(blockIdx.x / split);
+    }
+    __syncthreads();
+    const int expert = shared_word[2];
+    if (expert < 0) return;   // no such tile: the whole cluster leaves
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(shared_word)),
+                     "r"(C::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const int rows = shared_word[4];
+    const int mt = (rows + NT - 1) / NT;
+    const int tm = shared_word[5] % mt, tn = shared_word[5] / mt;
+    const int row0 = shared_word[3] + tm * NT;        // first token
+    const int ntok = min(NT, rows - tm * NT);
+    const int kb = (int)((int64_t)p.ks_total * rank / (int)split);
+    const int ke = (int)((int64_t)p.ks_total * (rank + 1) / (int)split);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = (uint32_t)shared_word[0];
+
+    if (warp == 0) {
+        if (lane == 0 && kb < ke) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmX)) : "memory");
+            // Static weights: the first stages' weight tiles are requested
+            // before the dependency wait, their token tiles after it.
+            int pre = 0;
+            if (!p.offsets && p.b_static)
+                for (; pre < STAGES && kb + pre < ke; ++pre) {
+                    mbar_arrive_expect_tx(FULL(pre), C::STAGE_BYTES);
+                    tma_load_3d(&tmW, FULL(pre), smem0 + pre * C::STAGE_BYTES, (kb + pre) * I8_BK, tn * I8_BM, expert);
+                }
+            pdl_wait();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int ks = kb; ks < ke; ++ks) {
+                const uint32_t st = smem0 + stage * C::STAGE_BYTES;
+                if (ks - kb >= pre) {
+                    if (!wait_fast(EMPTY(stage), phase ^ 1u, abort_flag, ERR_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(FULL(stage), C::STAGE_BYTES);
+                    tma_load_3d(&tmW, FULL(stage), st, ks * I8_BK, tn * I8_BM, expert);
+                }
+                tma_load_2d(&tmX, FULL(stage), st + C::OFF_T, ks * I8_BK, row0);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            pdl_trigger();
+            if (!ok || *abort_flag) spin_ns(200000);   // loads in flight land before the memory is used again
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && kb < ke) {
+            const uint64_t adesc0 = desc_sw128(smem0);
+            const uint64_t bdesc0 = desc_sw128(smem0 + C::OFF_T);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int ks = kb; ks < ke; ++ks) {
+                if (!wait_fast(FULL(stage), phase, abort_flag, ERR_FULL)) break;
+                tc_fence_after();
+                const uint64_t step = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+#pragma unroll
+                for (int j = 0; j < I8_BK / I8_MMA_K; ++j)
+                    mma_i8(tmem_base, adesc0 + step + 2 * j, bdesc0 + step + 2 * j, idesc_i8(I8_BM, NT),
+                           (ks > kb || j > 0) ? 1u : 0u);
+                tc_commit(EMPTY(stage));
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            // completes when every MMA issued here has
+            tc_commit(acc_full);
+        }
+        __syncwarp();
+    } else {
+        pdl_wait();   // the scales and D are touched below
+        const int q = warp & 3;   // tensor-memory lane quadrant: channels [32 q, 32 q + 32)
+        const uint32_t dst = smem0 + (uint32_t)(q * 32 + lane) * 4u;
+        const bool have = kb < ke && warp_wait(acc_full, 0, abort_flag, ERR_ACC_FULL);
+        tc_fence_after();
+        // Every stage has been read by then (the MMAs are complete), so the
+        // sums take their place.
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+            if (c >= ntok) break;
+            uint32_t r[16];
+            if (have) {
+                tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
+                tmem_wait_ld(r);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (uint32_t)(c + i) * (I8_BM * 4)), "r"(r[i]) : "memory");
+        }
+    }
+    if (warp < 2) pdl_wait();   // these warps' threads read scales and write D below as well
+    tc_fence_before();
+    __syncwarp();
+    if (split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS)
+                     : "memory");
+
+    // This CTA's channels: [128 rank / S, 128 (rank + 1) / S) of the tile, four a thread.
+    const int pieces = I8_BM / 4 / (int)split;
+    const int64_t chan_base = (int64_t)expert * p.N;
+    for (int i = threadIdx.x; i < ntok * pieces; i += kSwapThreads) {
+        const int tok = i / pieces;
+        const int ch = (rank * pieces + i % pieces) * 4;   // within the tile
+        const int n = tn * I8_BM + ch;
+        if (n >= p.N) continue;
+        const uint32_t at = smem0 + (uint32_t)(tok * I8_BM + ch) * 4u;
+        int4 sum = make_int4(0, 0, 0, 0);
+        for (uint32_t r = 0; r < split; ++r) {
+            const int4 v = ld_cluster_v4(map_to_rank(at, r));
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
+        const int64_t row = (int64_t)row0 + tok;
+        const float sa = __ldcg(p.sa + row);
+        const int acc[4] = {sum.x, sum.y, sum.z, sum.w};
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = n + j < p.N;
+            const float sb = in ? __ldcg(p.sb + chan_base + n + j) : 0.0f;
+            const float bias = in && p.bias ? __ldcg(p.bias + chan_base + n + j) : 0.0f;
+            v[j] = scaled(acc[j], sa, sb, bias);
+        }
+        const uint32_t lo = pack16<HALF>(v[0], v[1]), hi = pack16<HALF>(v[2], v[3]);
+        uint16_t* d = p.D + row * p.ldd + n;
+        if (n + 4 <= p.N) {
+            *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+        } else {
+            d[0] = (uint16_t)lo;
+            if (n + 1 < p.N) d[1] = (uint16_t)(lo >> 16);
+            if (n + 2 < p.N) d[2] = (uint16_t)hi;
+        }
+    }
+    if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums
+}
+
+// ------------------------------------------------------------------------
+// Many tokens: a cluster of two CTAs computes a 256 x BN tile with pair MMAs
+// (M = 256, N = BN): each CTA stages its own 128 rows of A and half of the
+// tile's B rows.  Two accumulators in tensor memory, so that a tile's
+// epilogue runs beside the next tile's MMAs.
+//   warp 0      producer (both CTAs; loads complete on the leader's full[s])
+//   warp 1      MMA issue (leader): passes a stage's named barrier, issues
+//               four MMAs and the commit that releases the stage in both
+//               CTAs; it touches no mbarrier, since a probe between two
+//               stages' MMAs leaves the tensor pipe idle
+//   warp 2      gatekeeper (leader): waits for the accumulator's release and
+//               for each stage, then opens the stage's named barrier
+//   warp 3      grouped: the tile list from the offsets
+//   warps 4-11  epilogue: two warps a tensor-memory lane quadrant, BN / 2
+//               columns each; scales, bias, 16 bits, 32 x 32 blocks through
+//               shared memory and TMA stores (row by row where a block
+//               reaches past its expert's last row)
+// Every wait is bounded; a CTA that gives up records it in the error word.
+// ------------------------------------------------------------------------
+constexpr int kI8PairThreads = 384;
+constexpr int kI8EpiWarps = 8;
+
+template <int BN>
+struct I8PairCfg {
+    static constexpr int B_BYTES = BN / 2 * I8_BK;
+    static constexpr int STAGE_BYTES = I8_TILE + B_BYTES;
+    static constexpr int STAGES = BN == 256 ? 6 : 8;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int EPI_BLOCK = 32 * 64;                 // 32 rows x 32 columns of 16 bits
+    static constexpr int WARP_COLS = BN / 2;                  // columns of an epilogue warp
+    static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
+    static constexpr int OFF_SCALE = OFF_EPI + kI8EpiWarps * EPI_BLOCK;            // sB and bias of the warp's columns
+    static constexpr int OFF_LIST = OFF_SCALE + kI8EpiWarps * 2 * 128 * 4;         // experts' first tiles and bounds
+    static constexpr int OFF_BARS = OFF_LIST + 2 * (kMaxExperts + 2) * 4;
+    static constexpr int NBARS = 2 * STAGES + 5;
+    static constexpr int SMEM = OFF_BARS + 256 + 1024;
+    static_assert(NBARS * 8 + 8 <= 256, "barrier area");
+    static_assert(OFF_BARS % 16 == 0, "barrier alignment");
+    static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+template <int BN, bool HALF, bool GROUPED>
+__global__ void __launch_bounds__(kI8PairThreads, 1)
+int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmD, const I8Params p)
+{
+    using C = I8PairCfg<BN>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+    // [0,S) full (leader), [S,2S) empty, [2S..2S+1] acc_full, [2S+2..2S+3] acc_empty (leader), [2S+4] drain
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* list = reinterpret_cast<int*>(smem + C::OFF_LIST);   // [E + 1] first tile of each expert
+    int* bound = list + kMaxExperts + 2;                      // [E + 1] its first row
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const uint32_t smem0 = smem_u32(smem);
+    const uint32_t bar0 = smem_u32(bars);
+    auto FULL = [&](int s) { return bar0 + 8u * s; };
+    auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto ACC_FULL = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto ACC_EMPTY = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    const uint32_t drain = bar0 + 8u * (2 * STAGES + 4);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(FULL(s), 1);
+            mbar_init(EMPTY(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(ACC_FULL(b), 1);
+            mbar_init(ACC_EMPTY(b), 2 * kI8EpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)),
+                     "r"(C::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (GROUPED && warp == 3) {
+        pdl_wait();
+        int reached = 0, seen = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            int first, end;
+            expert_bounds(p, e0, lane, reached, first, end);
+            const int tiles = (end - first + 255) / 256 * p.tiles_n;
+            const int upto = warp_scan_add(tiles, lane);
+            if (e0 + lane < p.E) {
+                list[e0 + lane] = seen + upto - tiles;
+                bound[e0 + lane] = first;
+                if (e0 + lane == p.E - 1) {
+                    list[p.E] = seen + upto;
+                    bound[p.E] = end;
+                }
+            }
+            seen += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        }
+    }
+    tc_fence_before();
+    cluster_sync();   // barriers of both CTAs initialised, TMEM allocated, tile list written
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int pair = blockIdx.x >> 1;
+    const int npairs = gridDim.x >> 1;
+    const int tiles = GROUPED ? list[p.E] : (p.M + 255) / 256 * p.tiles_n;
+    // Expert, first row and channel of tile t, and the end of the expert's
+    // rows.  Within an expert groups of raster_gm consecutive M tiles sweep
+    // the N tiles together (M fastest), so that a group's A rows stay in L2
+    // while B streams past them once.
+    struct Place {
+        int e, row, col, row_end;
+    };
+    auto locate = [&](int t) {
+        Place w;
+        int lo = 0, base = 0, end = p.M;
+        if (GROUPED) {
+            int hi = p.E;   // list[lo] <= t < list[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (list[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            t -= list[lo];
+            base = bound[lo];
+            // an empty expert has no tile, so lo is the one that holds t; its
+            // rows end where the next expert's begin
+            end = bound[lo + 1];
+        }
+        const int tiles_m = (end - base + 255) >> 8;
+        const int span = p.raster_gm * p.tiles_n;
+        const int grp = t / span, in = t - grp * span;
+        const int m0 = grp * p.raster_gm;
+        const int gm = min(tiles_m - m0, p.raster_gm);
+        w.e = lo;
+        w.row = base + (m0 + in % gm) * 256;
+        w.col = in / gm * BN;
+        w.row_end = end;
+        return w;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            pdl_wait();
+            for (int t = pair; ok && t < tiles; t += npairs) {
+                const Place w = locate(t);
+                const int ya = w.row + (int)rank * I8_BM;
+                const int yb = w.col + (int)rank * (BN / 2);
+                for (int ks = 0; ks < p.ks_total; ++ks) {
+                    if (!wait_fast(EMPTY(stage), phase ^ 1u, abort_flag, ERR_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_arrive_expect_tx(FULL(stage), 2u * C::STAGE_BYTES);
+                    const uint32_t full = map_to_rank(FULL(stage), 0);
+                    const uint32_t st = smem0 + stage * C::STAGE_BYTES;
+                    tma_load_3d_pair(&tmA, full, st, ks * I8_BK, ya, 0);
+                    tma_load_3d_pair(&tmB, full, st + I8_TILE, ks * I8_BK, yb, w.e);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            pdl_trigger();
+            if (!ok || *abort_flag) spin_ns(200000);   // loads in flight land before the CTAs meet
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader) {
+            const uint64_t adesc0 = desc_sw128(smem0);
+            const uint64_t bdesc0 = desc_sw128(smem0 + I8_TILE);
+            int stage = 0, buf = 0;
+            for (int t = pair; t < tiles; t += npairs) {
+                const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
+                for (int ks = 0; ks < p.ks_total; ++ks) {
+                    named_bar_sync(1 + stage, 64);
+                    if (lane == 0) {
+                        tc_fence_after();
+                        const uint64_t step = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+#pragma unroll
+                        for (int j = 0; j < I8_BK / I8_MMA_K; ++j)
+                            mma_i8_pair(acc, adesc0 + step + 2 * j, bdesc0 + step + 2 * j, idesc_i8(256, BN),
+                                        (ks > 0 || j > 0) ? 1u : 0u);
+                        tc_commit_pair_both(EMPTY(stage));
+                    }
+                    __syncwarp();
+                    if (++stage == STAGES) stage = 0;
+                }
+                if (lane == 0) tc_commit_pair_both(ACC_FULL(buf));
+                __syncwarp();
+                buf ^= 1;
+            }
+            if (lane == 0) {
+                // every pair MMA issued here has completed before the TMEM is freed
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain)
+                             : "memory");
+                wait_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // After a wait that gave up the gatekeeper goes on opening barriers
+        // without waiting, so that the MMA warp is never left blocked.
+        if (leader) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles; t += npairs) {
+                if (ok && !warp_wait(ACC_EMPTY(buf), acc_phase ^ 1u, abort_flag, ERR_ACC_EMPTY)) ok = false;
+                for (int ks = 0; ks < p.ks_total; ++ks) {
+                    if (ok && !warp_wait(FULL(stage), phase, abort_flag, ERR_FULL)) ok = false;
+                    named_bar_arrive(1 + stage, 64);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                buf ^= 1;
+                if (buf == 0) acc_phase ^= 1u;
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3;                  // tensor-memory lane quadrant
+        const int half = (warp - 4) >> 2;        // columns [BN/2 half, BN/2 half + BN/2)
+        const int eb = warp - 4;
+        float* sbs = reinterpret_cast<float*>(smem + C::OFF_SCALE) + eb * 256;
+        float* bis = sbs + 128;
+        const uint32_t blk = smem0 + C::OFF_EPI + eb * C::EPI_BLOCK;
+        const uint32_t my_row = blk + lane * 64;
+        const int sw = (lane >> 1) & 3;
+        pdl_wait();
+        uint32_t acc_phase = 0;
+        int buf = 0;
+        for (int t = pair; t < tiles; t += npairs) {
+            const Place w = locate(t);
+            const int y0 = w.row + (int)rank * I8_BM + q * 32;
+            const int col0 = w.col + half * C::WARP_COLS;
+            const float sa = y0 + lane < w.row_end ? __ldcg(p.sa + y0 + lane) : 0.0f;
+            const int64_t chan_base = (int64_t)w.e * p.N;
+#pragma unroll
+            for (int i = 0; i < C::WARP_COLS; i += 32) {
+                const int n = col0 + i + lane;
+                sbs[i + lane] = n < p.N ? __ldcg(p.sb + chan_base + n) : 0.0f;
+                bis[i + lane] = n < p.N && p.bias ? __ldcg(p.bias + chan_base + n) : 0.0f;
+            }
+            __syncwarp();
+            if (!warp_wait(ACC_FULL(buf), acc_phase, abort_flag, ERR_ACC_FULL)) break;
+            tc_fence_after();
+            const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + half * C::WARP_COLS);
+            // 32 columns at a time; the next columns' load overlaps this one's arithmetic
+            constexpr int NC = C::WARP_COLS / 32;
+            uint32_t ra[32], rb[32];
+            auto store = [&](const uint32_t (&r)[32], int c) {
+                const int x0 = col0 + c * 32;
+                if (y0 >= w.row_end || x0 >= p.N) return;
+                uint32_t packed[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 s4 = *reinterpret_cast<const float4*>(sbs + c * 32 + 4 * i);
+                    const float4 b4 = *reinterpret_cast<const float4*>(bis + c * 32 + 4 * i);
+                    packed[2 * i] = pack16<HALF>(scaled((int)r[4 * i], sa, s4.x, b4.x),
+                                                 scaled((int)r[4 * i + 1], sa, s4.y, b4.y));
+                    packed[2 * i + 1] = pack16<HALF>(scaled((int)r[4 * i + 2], sa, s4.z, b4.z),
+                                                     scaled((int)r[4 * i + 3], sa, s4.w, b4.w));
+                }
+                // A TMA store clips at the tensor's edge in whole 16 bytes, so
+                // the last columns of an N that is not a multiple of 8 are
+                // stored one by one; as are the rows of a block that holds
+                // the next expert's first ones too.
+                const bool whole = (!GROUPED || y0 + 32 <= w.row_end) && (x0 + 32 <= p.N || (p.N & 7) == 0);
+                if (whole) {
+                    // 64-byte rows, 16-byte piece j of row r at j ^ ((r >> 1) & 3): the 64-byte swizzle
+                    if (lane == 0) bulk_wait_read_all();   // the block's previous store has read it
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(my_row + ((j ^ sw) << 4)),
+                                     "r"(packed[4 * j]), "r"(packed[4 * j + 1]), "r"(packed[4 * j + 2]),
+                                     "r"(packed[4 * j + 3])
+                                     : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) tma_store_2d(&tmD, blk, x0, y0);
+                } else if (y0 + lane < w.row_end) {
+                    uint16_t* d = p.D + (int64_t)(y0 + lane) * p.ldd + x0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (x0 + 8 * j + 8 <= p.N) {
+                            *reinterpret_cast<uint4*>(d + 8 * j) = make_uint4(packed[4 * j], packed[4 * j + 1],
+                                                                              packed[4 * j + 2], packed[4 * j + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (x0 + 8 * j + i < p.N)
+                                    d[8 * j + i] = (uint16_t)(packed[4 * j + (i >> 1)] >> (16 * (i & 1)));
+                        }
+                    }
+                }
+            };
+            tmem_ld32(trow, ra);
+            tmem_wait_ld(ra);
+#pragma unroll
+            for (int c = 0; c < NC; c += 2) {
+                tmem_ld32(trow + (c + 1) * 32, rb);
+                store(ra, c);
+                tmem_wait_ld(rb);
+                if (c + 2 < NC) tmem_ld32(trow + (c + 2) * 32, ra);
+                if (c + 2 >= NC) {
+                    // every column is in registers: hand the accumulator back
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader)
+                            mbar_arrive(ACC_EMPTY(buf));
+                        else
+                            mbar_arrive_cluster_relaxed(map_to_rank(ACC_EMPTY(buf), 0));
+                    }
+                }
+                store(rb, c + 1);
+                if (c + 2 < NC) tmem_wait_ld(ra);
+            }
+            __syncwarp();   // the scales' memory is written again for the next tile
+            buf ^= 1;
+            if (buf == 0) acc_phase ^= 1u;
+        }
+        if (lane == 0) bulk_wait_all();   // every store of D has completed
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    cluster_sync();   // all pair MMAs done, both epilogues finished reading TMEM
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS)
+                     : "memory");
+}
+
+// ------------------------------------------------------------------------
+// Host side
+// ------------------------------------------------------------------------
+// [depth x rows x cols] bytes, boxes of 128 bytes x box_rows, 128-byte
+// swizzle, zero outside.
+bool make_map_i8(CUtensorMap* m, const void* base, int64_t depth, int64_t rows, int64_t cols, int64_t ld,
+                 int64_t stride, int box_rows)
+{
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+    cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
+    cuuint32_t box[3] = {(cuuint32_t)I8_BK, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map_i8_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+{
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {(cuuint32_t)I8_BK, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// D [rows x cols] of 16 bits, stored in 32 x 32 boxes with the 64-byte swizzle.
+bool make_map_d16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld)
+{
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {32, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Raises a kernel's dynamic shared-memory limit once per device; each caller
+// passes a mask of its own.
+cudaError_t raise_smem(const void* kernel, int bytes, uint64_t& done_mask)
+{
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && ((done_mask >> dev) & 1ull)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done_mask |= 1ull << dev;
+    return e;
+}
+
+void launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], unsigned grid, unsigned threads,
+                   unsigned cluster, size_t smem, cudaStream_t s)
+{
+    cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+}
+
+I8Params params_of(const Int8GemmArgs& a, int bn)
+{
+    I8Params p;
+    p.sa = a.sA;
+    p.sb = a.sB;
+    p.bias = a.bias;
+    p.D = a.D;
+    p.ldd = a.ldd;
+    p.M = (int32_t)a.M;
+    p.N = (int32_t)a.N;
+    p.ks_total = (int32_t)((a.K + I8_BK - 1) / I8_BK);
+    p.tiles_n = (int32_t)((a.N + bn - 1) / bn);
+    p.raster_gm = 1;
+    p.E = (int32_t)a.E;
+    p.offsets = a.offsets;
+    p.b_static = a.b_static ? 1 : 0;
+    return p;
+}
+
+template <int NT, bool HALF>
+cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, cudaStream_t s)
+{
+    using C = SwapCfg<NT>;
+    CUtensorMap tw = {}, tx = {};
+    if (a.K > 0 && (!make_map_i8(&tw, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, I8_BM) ||
+                    !make_map_i8_2d(&tx, a.A, a.M, a.K, a.lda, NT))) {
+        set_last_error("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
+        return cudaErrorInvalidValue;
+    }
+    static uint64_t done = 0;
+    auto kern = int8_swap_kernel<NT, HALF>;
+    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), C::SMEM, done);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        launch_config(cfg, attr, (unsigned)(clusters * split), kSwapThreads, (unsigned)split, C::SMEM, s);
+        e = cudaLaunchKernelEx(&cfg, kern, tw, tx, params_of(a, I8_BM));
+    }
+    if (e != cudaSuccess) set_last_error("INT8 GEMM launch (few tokens)", e);
+    return e;
+}
+
+template <int BN, bool HALF, bool GROUPED>
+cudaError_t launch_pair(const Int8GemmArgs& a, int64_t tiles, int sm_count, cudaStream_t s)
+{
+    using C = I8PairCfg<BN>;
+    CUtensorMap ta, tb, td;
+    if (!make_map_i8(&ta, a.A, 1, a.M, a.K, a.lda, a.lda, I8_BM) ||
+        !make_map_i8(&tb, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, BN / 2) ||
+        !make_map_d16(&td, a.D, a.M, a.N, a.ldd)) {
+        set_last_error("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
+        return cudaErrorInvalidValue;
+    }
+    I8Params p = params_of(a, BN);
+    // M tiles per group: as many as hold kI8GroupBytes of A, all of them when
+    // A fits in half of the L2 cache
+    const int64_t tile_bytes = 256 * a.K, tiles_m = (a.M + 255) / 256;
+    int64_t rg = tiles_m;
+    if (tile_bytes * tiles_m > 2 * kI8GroupBytes) rg = (kI8GroupBytes + tile_bytes / 2) / tile_bytes;
+    p.raster_gm = (int32_t)(rg < 1 ? 1 : rg > tiles_m ? tiles_m : rg);
+    static uint64_t done = 0;
+    auto kern = int8_pair_kernel<BN, HALF, GROUPED>;
+    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), C::SMEM, done);
+    if (e == cudaSuccess) {
+        const int64_t pairs = sm_count / 2;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        launch_config(cfg, attr, 2u * (unsigned)(tiles < pairs ? tiles : pairs), kI8PairThreads, 2, C::SMEM, s);
+        e = cudaLaunchKernelEx(&cfg, kern, ta, tb, td, p);
+    }
+    if (e != cudaSuccess) set_last_error("INT8 GEMM launch (CTA pairs)", e);
+    return e;
+}
+
+template <int NT>
+cudaError_t launch_swap_t(const Int8GemmArgs& a, int split, int64_t clusters, cudaStream_t s)
+{
+    return a.half_out ? launch_swap<NT, true>(a, split, clusters, s) : launch_swap<NT, false>(a, split, clusters, s);
+}
+
+template <int BN>
+cudaError_t launch_pair_t(const Int8GemmArgs& a, int64_t tiles, int sm_count, cudaStream_t s)
+{
+    if (a.offsets)
+        return a.half_out ? launch_pair<BN, true, true>(a, tiles, sm_count, s)
+                          : launch_pair<BN, false, true>(a, tiles, sm_count, s);
+    return a.half_out ? launch_pair<BN, true, false>(a, tiles, sm_count, s)
+                      : launch_pair<BN, false, false>(a, tiles, sm_count, s);
+}
+
+// Token tiles of `nt` rows that a launch may need: a grouped one knows only
+// the number of rows and experts.
+int64_t most_token_tiles(const Int8GemmArgs& a, int nt)
+{
+    if (!a.offsets) return (a.M + nt - 1) / nt;
+    return a.M / nt + (a.E < a.M ? a.E : a.M);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo& dev, cudaStream_t s)
+{
+    const int64_t per_expert = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
+    bool swap = kernel == FP4_GEMM_DECODE || a.K == 0;
+    if (kernel == FP4_GEMM_AUTO) swap = swap || per_expert <= 128;
+    if (swap) {
+        const int nt = per_expert <= 16 ? 16 : per_expert <= 32 ? 32 : per_expert <= 64 ? 64 : 128;
+        const int64_t tiles_n = (a.N + I8_BM - 1) / I8_BM;
+        const int64_t clusters = most_token_tiles(a, nt) * tiles_n;
+        const int64_t ks = (a.K + I8_BK - 1) / I8_BK;
+        int split = 1;
+        while (split < 8 && clusters * split * 2 <= 2 * dev.sm_count && ks >= 4 * split) split *= 2;
+        if (nt == 16) return launch_swap_t<16>(a, split, clusters, s);
+        if (nt == 32) return launch_swap_t<32>(a, split, clusters, s);
+        if (nt == 64) return launch_swap_t<64>(a, split, clusters, s);
+        return launch_swap_t<128>(a, split, clusters, s);
+    }
+    const int64_t tm = most_token_tiles(a, 256);
+    const int64_t t256 = tm * ((a.N + 255) / 256), t128 = tm * ((a.N + 127) / 128);
+    if (t256 >= dev.sm_count / 2) return launch_pair_t<256>(a, t256, dev.sm_count, s);
+    return launch_pair_t<128>(a, t128, dev.sm_count, s);
+}
+
+cudaError_t read_and_clear_int8_error_word(unsigned int* word)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_fp4_error_word, sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    if (*word) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_fp4_error_word, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
+}  // namespace fp4

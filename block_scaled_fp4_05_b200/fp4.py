@@ -5,6 +5,7 @@ current torch stream to the C ABI; all arithmetic runs in the library's CUDA
 kernels.  There is no fallback: if ``libfp4.so`` is missing or a call fails,
 an exception is raised.
 """
+import contextlib
 import ctypes
 import os
 import re
@@ -14,6 +15,7 @@ import torch
 NVFP4, MXFP4, P1E8 = 0, 1, 2   # P1E8: 16-element blocks, E8M0 scale under S_global (quantizer only)
 ROWWISE, COLWISE = 0, 1
 GEMM_AUTO, GEMM_PREFILL, GEMM_DECODE = 0, 1, 2
+BF16, FP16 = 0, 1   # fp4_dtype: 16-bit types of the INT8 entry points
 GEMM_B_STATIC = 0x100   # flag: B / sB not written by a kernel still running on the stream
 
 FP4_OK = 0
@@ -91,6 +93,13 @@ def lib():
         L.fp4_gemm_decode_dynamic.argtypes = [P, i64, P, P, P, i64, i64, i64, P, i64, P, P, P, sz, st]
         L.fp4_gemm_decode_noalloc.restype = c.c_int
         L.fp4_gemm_decode_noalloc.argtypes = [c.c_int, P, P, P, P, i64, i64, i64, P, P, i64, st]
+        L.fp4_quantize_int8.restype = c.c_int
+        L.fp4_quantize_int8.argtypes = [P, c.c_int, i64, i64, i64, P, i64, P, i64, P, st]
+        L.fp4_gemm_int8.restype = c.c_int
+        L.fp4_gemm_int8.argtypes = [P, i64, P, P, i64, P, i64, i64, i64, P, c.c_int, P, i64, c.c_int, st]
+        L.fp4_gemm_int8_grouped.restype = c.c_int
+        L.fp4_gemm_int8_grouped.argtypes = [P, i64, P, P, i64, i64, P, P, i64, i64, i64, i64, P, c.c_int, P,
+                                            i64, c.c_int, st]
         _lib = L
     return _lib
 
@@ -322,6 +331,131 @@ def bind_gemm_decode_dynamic(x, W, sW, gsW, D, gs_out, alpha_out, workspace, str
                      workspace.numel() * workspace.element_size(), _stream(stream))
 
 
+# ---------------------------------------------------------------------------
+# INT8 layers: one scale per token (row of A) and per output channel (row of B)
+# ---------------------------------------------------------------------------
+_DTYPE16 = {torch.bfloat16: BF16, torch.float16: FP16}
+
+
+def _i8_device(first, *rest):
+    """The current device, on which every tensor has to lie."""
+    dev = torch.cuda.current_device()
+    for t in (first,) + rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("every tensor has to be on the current device (cuda:%d): got one on %s" % (dev, t.device))
+
+
+def _i8_ld(t, what, dtypes, unit):
+    """Leading dimension of matrix t (the last two dimensions).  That of a
+    single row, or of rows without elements, is never used: it counts as the
+    next multiple of `unit`."""
+    if t.dtype not in dtypes:
+        raise TypeError("%s has type %s" % (what, t.dtype))
+    rows, cols = t.shape[-2], t.shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError("%s needs unit column stride" % what)
+    return t.stride(-2) if rows > 1 and cols > 0 else (cols + unit - 1) // unit * unit
+
+
+def _i8_vector(t, what, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError("%s has type %s, not %s" % (what, t.dtype, dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s has to be contiguous with shape %s: got %s" % (what, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+_I8 = (torch.int8,)
+
+
+def _quantize_int8_args(x, codes, scales, row_index, stream):
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x and codes are matrices")
+    _i8_device(x, codes, scales, row_index)
+    rows, cols = codes.shape
+    if x.shape[1] != cols or (row_index is None and x.shape[0] != rows):
+        raise ValueError("codes of shape %s do not fit x of shape %s" % (tuple(codes.shape), tuple(x.shape)))
+    ld = _i8_ld(x, "x", _DTYPE16, 8)
+    return (x.data_ptr(), _DTYPE16[x.dtype], x.shape[0], cols, ld,
+            None if row_index is None else _i8_vector(row_index, "row_index", torch.int32, (rows,)), rows,
+            codes.data_ptr(), _i8_ld(codes, "codes", _I8, 16), _i8_vector(scales, "scales", torch.float32, (rows,)),
+            _stream(stream))
+
+
+def fp4_quantize_int8(x, codes, scales, row_index=None, stream=None):
+    """Per-row INT8 quantization of x [R x C] (bf16 or fp16) into codes (int8)
+    and scales (float32): scales = amax / 127, codes = 127 x / amax rounded to
+    nearest even.  With row_index (int32) output row r is x[row_index[r]]."""
+    st = lib().fp4_quantize_int8(*_quantize_int8_args(x, codes, scales, row_index, stream))
+    if st != FP4_OK:
+        _check(st, "fp4_quantize_int8")
+
+
+def bind_quantize_int8(x, codes, scales, row_index=None, stream=None):
+    call = BoundCall("fp4_quantize_int8", *_quantize_int8_args(x, codes, scales, row_index, stream))
+    call.keep = (x, codes, scales, row_index)
+    return call
+
+
+def _gemm_int8_args(A, sA, B, sB, D, bias, kernel, stream):
+    if A.dim() != 2 or B.dim() != 2 or D.dim() != 2:
+        raise ValueError("A, B and D are matrices")
+    _i8_device(A, sA, B, sB, D, bias)
+    (M, K), N = A.shape, B.shape[0]
+    if B.shape[1] != K or D.shape[0] != M or D.shape[1] != N:
+        raise ValueError("shapes do not fit: A %s, B %s, D %s" % (tuple(A.shape), tuple(B.shape), tuple(D.shape)))
+    ldd = _i8_ld(D, "D", _DTYPE16, 8)
+    return (A.data_ptr(), _i8_ld(A, "A", _I8, 16), _i8_vector(sA, "sA", torch.float32, (M,)),
+            B.data_ptr(), _i8_ld(B, "B", _I8, 16), _i8_vector(sB, "sB", torch.float32, (N,)), M, N, K,
+            None if bias is None else _i8_vector(bias, "bias", torch.float32, (N,)),
+            _DTYPE16[D.dtype], D.data_ptr(), ldd, int(kernel), _stream(stream))
+
+
+def fp4_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
+    """D [M x N] (bf16 or fp16) = (A @ B^T) * sA[:, None] * sB + bias for int8
+    A [M x K] and B [N x K]: exact integer sums, scaled and rounded once."""
+    st = lib().fp4_gemm_int8(*_gemm_int8_args(A, sA, B, sB, D, bias, kernel, stream))
+    if st != FP4_OK:
+        _check(st, "fp4_gemm_int8")
+
+
+def bind_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
+    call = BoundCall("fp4_gemm_int8", *_gemm_int8_args(A, sA, B, sB, D, bias, kernel, stream))
+    call.keep = (A, sA, B, sB, D, bias)
+    return call
+
+
+def _gemm_int8_grouped_args(A, sA, B, sB, offsets, D, bias, kernel, stream):
+    if A.dim() != 2 or B.dim() != 3 or D.dim() != 2:
+        raise ValueError("A and D are matrices, B is [experts x N x K]")
+    _i8_device(A, sA, B, sB, offsets, D, bias)
+    (T, K), (E, N, KB) = A.shape, B.shape
+    if KB != K or D.shape[0] != T or D.shape[1] != N:
+        raise ValueError("shapes do not fit: A %s, B %s, D %s" % (tuple(A.shape), tuple(B.shape), tuple(D.shape)))
+    ldd, ldb = _i8_ld(D, "D", _DTYPE16, 8), _i8_ld(B, "B", _I8, 16)
+    return (A.data_ptr(), _i8_ld(A, "A", _I8, 16), _i8_vector(sA, "sA", torch.float32, (T,)),
+            B.data_ptr(), ldb, B.stride(0) if E > 1 and K > 0 else N * ldb, _i8_vector(sB, "sB", torch.float32, (E, N)),
+            _i8_vector(offsets, "offsets", torch.int32, (E + 1,)), E, T, N, K,
+            None if bias is None else _i8_vector(bias, "bias", torch.float32, (E, N)),
+            _DTYPE16[D.dtype], D.data_ptr(), ldd, int(kernel), _stream(stream))
+
+
+def fp4_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias=None, kernel=GEMM_AUTO, stream=None):
+    """fp4_gemm_int8 by expert: rows offsets[e] .. offsets[e + 1] of A and D
+    with B[e] [N x K], sB[e] and bias[e].  offsets (int32, E + 1) is read on
+    the device; rows of D in no group are left as they were."""
+    st = lib().fp4_gemm_int8_grouped(*_gemm_int8_grouped_args(A, sA, B, sB, offsets, D, bias, kernel, stream))
+    if st != FP4_OK:
+        _check(st, "fp4_gemm_int8_grouped")
+
+
+def bind_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias=None, kernel=GEMM_AUTO, stream=None):
+    call = BoundCall("fp4_gemm_int8_grouped",
+                     *_gemm_int8_grouped_args(A, sA, B, sB, offsets, D, bias, kernel, stream))
+    call.keep = (A, sA, B, sB, offsets, D, bias)
+    return call
+
+
 def fp4_get_device_status(stream=None):
     return lib().fp4_get_device_status(_stream(stream))
 
@@ -360,6 +494,58 @@ def gemm(fmt, A, sA, B, sB, K, alpha=None, kernel=GEMM_AUTO, out=None, workspace
             workspace = torch.zeros((nb,), dtype=torch.uint8, device=A.device)
     fp4_gemm(fmt, A, sA, B, sB, M, N, K, alpha, D, workspace, kernel, stream)
     return D
+
+
+def _padded(rows, cols, unit, dtype, device):
+    """[rows x cols] whose rows start at multiples of `unit` elements."""
+    return torch.empty((rows, (cols + unit - 1) // unit * unit), dtype=dtype, device=device)[:, :cols]
+
+
+def _on(stream):
+    """Makes `stream` the current one, so that what is allocated for a call
+    belongs to the stream that the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(int(stream)))
+
+
+def quantize_int8(x, row_index=None, stream=None):
+    """Per-row INT8 quantization of a bf16 or fp16 matrix; returns (codes, scales)."""
+    rows = x.shape[0] if row_index is None else row_index.shape[0]
+    with _on(stream):
+        codes = _padded(rows, x.shape[1], 16, torch.int8, x.device)
+        scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        fp4_quantize_int8(x, codes, scales, row_index)
+    return codes, scales
+
+
+def gemm_int8(A, sA, B, sB, bias=None, out=None, out_dtype=torch.bfloat16, kernel=GEMM_AUTO, stream=None):
+    """(A @ B^T) * sA[:, None] * sB + bias for int8 A, B; allocates the result unless given."""
+    with _on(stream):
+        D = out if out is not None else _padded(A.shape[0], B.shape[0], 8, out_dtype, A.device)
+        fp4_gemm_int8(A, sA, B, sB, D, bias, kernel)
+    return D
+
+
+def gemm_int8_grouped(A, sA, B, sB, offsets, bias=None, out=None, out_dtype=torch.bfloat16, kernel=GEMM_AUTO,
+                      stream=None):
+    """gemm_int8 by expert (fp4_gemm_int8_grouped); allocates the result unless
+    given (rows in no group are then undefined)."""
+    with _on(stream):
+        D = out if out is not None else _padded(A.shape[0], B.shape[1], 8, out_dtype, A.device)
+        fp4_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias, kernel)
+    return D
+
+
+def linear_int8(x, W, sW, bias=None, out=None, stream=None):
+    """x W^T + bias for a bf16 or fp16 activation x and a weight quantized ahead
+    of time by quantize_int8: the activation is quantized by token, then
+    multiplied; the result has x's type unless `out` is given.  The product
+    starts loading the weight while the quantizer still runs."""
+    with _on(stream):
+        codes, scales = quantize_int8(x)
+        return gemm_int8(codes, scales, W, sW, bias, out, x.dtype, GEMM_AUTO | GEMM_B_STATIC)
 
 
 # ---------------------------------------------------------------------------

@@ -102,6 +102,12 @@ typedef enum {
     FP4_GEMM_B_STATIC = 0x100
 } fp4_gemm_kernel;
 
+/* 16-bit floating types of the INT8 entry points' inputs and outputs. */
+typedef enum {
+    FP4_BF16 = 0,
+    FP4_FP16 = 1
+} fp4_dtype;
+
 /* Version of this ABI (incremented on any signature or contract change). */
 int fp4_abi_version(void);
 
@@ -409,6 +415,78 @@ fp4_status fp4_gemm_decode_noalloc(fp4_format fmt, const void* A, const void* sA
                                    const void* sB, int64_t M, int64_t N, int64_t K,
                                    const float* alpha, void* D, int64_t ldd,
                                    fp4_stream_t stream);
+
+/*
+ * 8-bit layers next to the 4-bit ones (no counterpart on the pages: they are
+ * for the layers of a model that do not bear four bits).  Per-row symmetric
+ * quantization to INT8: for each row
+ *   amax = max_k |x_k|,  scale = amax / 127 (FP32; 1.0 for a row of zeros),
+ *   code_k = 127 x_k / amax rounded to the nearest integer, halves to even
+ * (the codes of the exact quotient, in [-127, 127]).  Activations: a row is a
+ * token.  Weights [N x K]: a row is an output channel.
+ *   in        : device, rows_in x cols of in_dtype, leading dimension ld
+ *   row_index : device, `rows` source row numbers: output row r is the
+ *               quantized input row row_index[r] (the dispatch of tokens to
+ *               experts; a row may occur any number of times), or NULL:
+ *               output row r is input row r (rows == rows_in).  A number
+ *               outside [0, rows_in) gives a row of zeros with scale 1.
+ *   codes_out : device, rows x cols signed bytes, leading dimension ld_codes;
+ *               the bytes between cols and ld_codes are not written
+ *   scales_out: device, `rows` floats
+ * A row that holds an infinity or NaN gets scale NaN and codes 0, so that
+ * every product with it is NaN (an exception to the convention above).
+ * Requires ld % 8 == 0, ld_codes % 16 == 0, 16-byte aligned in and codes_out;
+ * cols may be any number (0: the scales are 1).  The outputs may not overlap
+ * the input.
+ */
+fp4_status fp4_quantize_int8(const void* in, fp4_dtype in_dtype, int64_t rows_in, int64_t cols, int64_t ld,
+                             const int32_t* row_index, int64_t rows, void* codes_out, int64_t ld_codes,
+                             float* scales_out, fp4_stream_t stream);
+
+/*
+ * D[m, n] = (sum_k A[m, k] B[n, k]) * sA[m] * sB[n] + bias[n]
+ * for signed 8-bit A and B: the sum is exact (32-bit integers on the tensor
+ * cores), the scales and the bias are applied in FP32 (the token's scale
+ * first), and the result is rounded once to out_dtype.
+ *   A : device, [M x K] bytes, leading dimension lda;  sA : M floats
+ *   B : device, [N x K] bytes, leading dimension ldb;  sB : N floats
+ *   bias : device, N floats, or NULL for none
+ *   D : device, [M x N] of out_dtype, leading dimension ldd; the elements
+ *       between N and ldd are not written
+ *   kernel : FP4_GEMM_AUTO; FP4_GEMM_PREFILL: CTA pairs, 256 x 256 or
+ *       256 x 128 tiles; FP4_GEMM_DECODE: weights on the 128-row side, K
+ *       split over a cluster.  Either takes any M; they give the same bits.
+ *       FP4_GEMM_B_STATIC may be OR-ed as for fp4_gemm (here for B alone).
+ * M, N and K may be any numbers (M == 0 or N == 0: a no-op; K == 0: the sums
+ * are 0) up to K <= 131071, above which a sum of products of -128 could leave
+ * 32 bits.  Requires lda, ldb % 16 == 0, ldd % 8 == 0, 16-byte aligned A, B
+ * and D.  The bytes of A and B between K and the leading dimension are not
+ * used.  No workspace: calls on several streams at once do not share
+ * anything.  Programmatic stream serialization as for fp4_gemm.
+ */
+fp4_status fp4_gemm_int8(const void* A, int64_t lda, const float* sA, const void* B, int64_t ldb,
+                         const float* sB, int64_t M, int64_t N, int64_t K, const float* bias,
+                         fp4_dtype out_dtype, void* D, int64_t ldd, fp4_gemm_kernel kernel, fp4_stream_t stream);
+
+/*
+ * fp4_gemm_int8 grouped by expert, with group sizes that only the device
+ * knows: the rows offsets[e] <= m < offsets[e + 1] of A, sA and D belong to
+ * expert e, whose weights are B + e * stride_b (bytes), scales sB + e * N and
+ * bias bias + e * N.  One launch for all experts; nothing is read back, so
+ * the call can be captured in a CUDA graph and replayed with other offsets.
+ *   offsets : device, E + 1 row numbers, non-decreasing, within [0, T]; read
+ *             when the kernel runs.  Others are taken as clamped to [0, T]
+ *             and raised to the largest one before them.
+ *   E : 0 <= E <= 512;  T : rows of A, sA and D
+ * Rows of D before offsets[0] and from offsets[E] on are left as they were;
+ * experts without rows cost nothing.  FP4_GEMM_AUTO chooses by T / E.
+ * Requires stride_b % 16 == 0 and stride_b >= (N - 1) * ldb + K, else as
+ * fp4_gemm_int8.
+ */
+fp4_status fp4_gemm_int8_grouped(const void* A, int64_t lda, const float* sA, const void* B, int64_t ldb,
+                                 int64_t stride_b, const float* sB, const int32_t* offsets, int64_t E,
+                                 int64_t T, int64_t N, int64_t K, const float* bias, fp4_dtype out_dtype,
+                                 void* D, int64_t ldd, fp4_gemm_kernel kernel, fp4_stream_t stream);
 
 /*
  * Synchronizes `stream`, then reports and clears the device error word of the

@@ -1,0 +1,154 @@
+"""INT8 entry points without a GPU: their refusals (checked in the order the
+header gives) and the tile lists that the grouped kernels form from the
+device's offsets, restated here."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from block_scaled_fp4_05_b200 import fp4
+
+P = ctypes.c_void_p
+A16 = P(1 << 20)       # 16-byte aligned dummy address (never dereferenced)
+A1 = P((1 << 20) + 1)
+A2 = P((1 << 20) + 2)
+
+
+def no_gpu():
+    import torch
+    return not torch.cuda.is_available()
+
+
+def test_new_symbols_are_declared_and_exported():
+    names = fp4.declared_symbols()
+    for n in ("fp4_quantize_int8", "fp4_gemm_int8", "fp4_gemm_int8_grouped"):
+        assert n in names and hasattr(fp4.lib(), n)
+
+
+# (in, dtype, rows_in, cols, ld, row_index, rows, codes, ld_codes, scales, stream)
+@pytest.mark.parametrize("args,want", [
+    ((A16, 2, 4, 64, 64, None, 4, A16, 64, A16, None), 1),          # type
+    ((A16, 0, -1, 64, 64, None, -1, A16, 64, A16, None), 1),        # negative
+    ((A16, 0, 4, 64, 56, None, 4, A16, 64, A16, None), 1),          # ld < cols
+    ((A16, 0, 4, 64, 64, None, 4, A16, 48, A16, None), 1),          # ld_codes < cols
+    ((A16, 0, 4, 64, 64, None, 5, A16, 64, A16, None), 1),          # rows differ without an index
+    ((None, 0, 4, 64, 64, None, 4, A16, 64, A16, None), 1),         # no input
+    ((A16, 0, 4, 64, 64, None, 4, None, 64, A16, None), 1),         # no codes
+    ((A16, 0, 4, 64, 64, None, 4, A16, 64, None, None), 1),         # no scales
+    ((A16, 0, 1 << 31, 64, 64, None, 1 << 31, A16, 64, A16, None), 2),
+    ((A1, 0, 4, 64, 64, None, 4, A16, 64, A16, None), 3),
+    ((A16, 0, 4, 64, 68, None, 4, A16, 64, A16, None), 3),          # ld % 8
+    ((A16, 0, 4, 64, 64, None, 4, A16, 72, A16, None), 3),          # ld_codes % 16
+    ((A16, 0, 4, 64, 64, None, 4, A1, 64, A16, None), 3),
+    ((A16, 0, 4, 64, 64, None, 4, A16, 64, A2, None), 3),
+    ((A16, 0, 4, 64, 64, A2, 8, A16, 64, A16, None), 3),
+    ((None, 0, 0, 64, 64, None, 0, None, 64, None, None), 0),       # no rows
+    ((A16, 0, 4, 61, 64, None, 4, A16, 64, A16, None), 6),          # valid, but no device here
+    ((None, 1, 0, 64, 64, A16, 4, A16, 64, A16, None), 6),          # every index is outside
+])
+def test_quantize_int8_refusals(args, want):
+    if want == 6 and not no_gpu():
+        pytest.skip("a device is present")
+    assert fp4.lib().fp4_quantize_int8(*args) == want
+
+
+GOOD = dict(A=A16, lda=64, sA=A16, B=A16, ldb=64, sB=A16, M=4, N=16, K=64, bias=None, out=0, D=A16, ldd=16, kernel=0)
+
+DENSE_REFUSALS = [
+    (dict(kernel=3), 1), (dict(kernel=0x200), 1), (dict(out=2), 1), (dict(M=-1), 1), (dict(K=-1), 1),
+    (dict(lda=48), 1), (dict(ldb=48), 1), (dict(ldd=8), 1), (dict(A=None), 1), (dict(B=None), 1),
+    (dict(D=None), 1), (dict(sA=None), 1), (dict(sB=None), 1),
+    (dict(K=131072, lda=131072, ldb=131072), 2), (dict(M=1 << 31), 2), (dict(lda=1 << 40), 2), (dict(ldd=1 << 39), 2),
+    (dict(M=1 << 30, N=1 << 20, ldd=1 << 20), 2),
+    (dict(lda=72), 3), (dict(ldb=72), 3), (dict(ldd=20), 3), (dict(A=A1), 3), (dict(B=A1), 3), (dict(D=A1), 3),
+    (dict(sA=A2), 3), (dict(sB=A2), 3), (dict(bias=A2), 3),
+    (dict(M=0), 0), (dict(N=0), 0),
+    (dict(), 6), (dict(K=0), 6), (dict(K=61, N=13), 6), (dict(kernel=0x102), 6), (dict(K=131071, lda=131072, ldb=131072), 6),
+]
+
+
+@pytest.mark.parametrize("change,want", DENSE_REFUSALS)
+def test_gemm_int8_refusals(change, want):
+    if want == 6 and not no_gpu():
+        pytest.skip("a device is present")
+    a = {**GOOD, **change}
+    assert fp4.lib().fp4_gemm_int8(a["A"], a["lda"], a["sA"], a["B"], a["ldb"], a["sB"], a["M"], a["N"], a["K"],
+                                   a["bias"], a["out"], a["D"], a["ldd"], a["kernel"], None) == want
+
+
+@pytest.mark.parametrize("change,want", DENSE_REFUSALS + [
+    (dict(E=-1), 1), (dict(offsets=None), 1), (dict(stride=-16), 1),
+    (dict(stride=15 * 64 + 48), 1),                       # experts would overlap
+    (dict(E=513), 2), (dict(stride=1 << 40), 2), (dict(stride=16 * 64 + 8), 3), (dict(offsets=A2), 3),
+    (dict(E=0), 0), (dict(E=0, offsets=None), 0), (dict(E=1, stride=0), 6), (dict(E=512), 6),
+])
+def test_gemm_int8_grouped_refusals(change, want):
+    if want == 6 and not no_gpu():
+        pytest.skip("a device is present")
+    a = {**GOOD, "offsets": A16, "E": 4, "stride": 1 << 39, **change}
+    assert fp4.lib().fp4_gemm_int8_grouped(a["A"], a["lda"], a["sA"], a["B"], a["ldb"], a["stride"], a["sB"],
+                                           a["offsets"], a["E"], a["M"], a["N"], a["K"], a["bias"], a["out"],
+                                           a["D"], a["ldd"], a["kernel"], None) == want
+
+
+# ---- the grouped kernels' bounds and tile lists, restated ----
+def expert_bounds(offsets, M):
+    """As 32 lanes form them, 32 experts at a time: first and end row of each."""
+    E, reached, out = len(offsets) - 1, 0, []
+    for e0 in range(0, E, 32):
+        lo, hi = np.zeros(32, np.int64), np.zeros(32, np.int64)
+        for lane in range(32):
+            if e0 + lane < E:
+                lo[lane] = min(max(offsets[e0 + lane], 0), M)
+                hi[lane] = min(max(offsets[e0 + lane + 1], 0), M)
+        top = np.maximum.accumulate(np.maximum(lo, hi))
+        before = np.concatenate([[0], top[:-1]])
+        first = np.maximum(np.maximum(before, reached), lo)
+        end = np.maximum(np.maximum(first, hi), reached)
+        out += [(int(f), int(g)) for f, g in list(zip(first, end))[: E - e0]]
+        reached = max(reached, int(top[31]))
+    return out
+
+
+def bounds_wanted(offsets, M):
+    b = np.maximum.accumulate(np.clip(np.asarray(offsets, np.int64), 0, M))
+    return list(zip(b[:-1].tolist(), b[1:].tolist()))
+
+
+def test_expert_bounds_are_clamped_and_never_decrease():
+    rng = np.random.default_rng(0)
+    for _ in range(300):
+        E, M = int(rng.integers(1, 130)), int(rng.integers(0, 500))
+        kind = rng.integers(3)
+        o = rng.integers(0, M + 1, E + 1)
+        if kind == 0:
+            o = np.sort(o)
+        elif kind == 1:
+            o = rng.integers(-(2 ** 31), 2 ** 31, E + 1)
+        assert expert_bounds(o.tolist(), M) == bounds_wanted(o, M)
+
+
+@pytest.mark.parametrize("nt", [16, 32, 64, 128, 256])
+def test_every_row_is_in_one_tile_and_the_bound_on_tiles_holds(nt):
+    rng = np.random.default_rng(1)
+    for _ in range(60):
+        E, M, tiles_n, rg = int(rng.integers(1, 80)), int(rng.integers(1, 3000)), int(rng.integers(1, 5)), int(rng.integers(1, 9))
+        o = np.sort(rng.integers(0, M + 1, E + 1))
+        bounds = expert_bounds(o.tolist(), M)
+        seen = np.zeros((M, tiles_n), np.int64)
+        listed = 0
+        for first, end in bounds:
+            mt = (end - first + nt - 1) // nt
+            listed += mt
+            for t in range(mt * tiles_n):
+                span = rg * tiles_n
+                grp, within = divmod(t, span)
+                m0 = grp * rg
+                gm = min(mt - m0, rg)
+                row, col = first + (m0 + within % gm) * nt, within // gm
+                seen[row:min(row + nt, end), col] += 1
+        inside = np.zeros(M, bool)
+        for first, end in bounds:
+            inside[first:end] = True
+        assert (seen[inside] == 1).all() and (seen[~inside] == 0).all()
+        assert listed <= M // nt + min(E, M)   # what the launch provides for

@@ -1,0 +1,460 @@
+"""GPU parity of the INT8 layers against their definitions in 64 bits.
+
+Quantizer: codes and scales are the exact quotient's and one FP32 division, so
+they are compared for equality.  Products: the integer sum is exact, so with
+p = |sum sA sB|, y = sum sA sB + bias and u the half step of the output type
+(2^-8 bf16, 2^-11 fp16):
+  FP32 steps: RN(sum) and its product with sA are off by 2^-24 each, the FMA
+  with sB and bias by 2^-24 of its result: at most 2^-24 (3 p + |y|);
+  the output's rounding adds u (|y| + that), or half of fp16's smallest
+  subnormal step, 2^-25.
+"""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_fp4_05_b200 import fp4
+from test_int8_abi import bounds_wanted
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+KERNELS = [fp4.GEMM_PREFILL, fp4.GEMM_DECODE, fp4.GEMM_AUTO]
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean():
+    yield
+    torch.cuda.synchronize()
+    assert fp4.fp4_get_device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# Quantizer
+# ---------------------------------------------------------------------------
+def quantize_definition(x):
+    """Codes and scales of finite rows, from numpy in 64 bits."""
+    v = x.double().cpu().numpy()
+    amax = np.abs(v).max(1) if v.shape[1] else np.zeros(v.shape[0])
+    safe = np.where(amax == 0, 1.0, amax)
+    codes = np.rint(127.0 * v / safe[:, None])
+    scales = np.where(amax == 0, np.float32(1), amax.astype(np.float32) / np.float32(127))
+    return codes.astype(np.int8), scales.astype(np.float32)
+
+
+def check_quantized(x, codes, scales, what=""):
+    want_codes, want_scales = quantize_definition(x)
+    assert np.array_equal(scales.cpu().numpy(), want_scales), what
+    got = codes.cpu().numpy()
+    bad = np.argwhere(got != want_codes)
+    assert bad.size == 0, "%s: %d codes differ, first %s: %s for %s" % (
+        what, len(bad), bad[0], got[tuple(bad[0])], want_codes[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (9, 8), (5, 255), (17, 256), (9, 257), (7, 513), (6, 1000),
+                                       (9, 1025), (2, 2048), (3, 2049), (2, 4096), (3, 4099), (1, 8192), (2, 8193),
+                                       (2, 16384), (2, 16391), (1, 32768), (2, 32771), (300, 64), (0, 64), (3, 0)])
+def test_quantize_shapes(dtype, rows, cols):
+    g = torch.Generator().manual_seed(rows * 1000 + cols)
+    x = (torch.randn(rows, cols + 40, generator=g) * torch.exp(3 * torch.randn(rows, 1, generator=g))).to(dtype).cuda()
+    x = x[:, : (cols + 40) // 8 * 8].contiguous()
+    v = x[:, 8:8 + cols]                       # a strided view: what is beside it may not matter
+    x[:, :8] = float("nan")
+    x[:, 8 + cols:] = float("inf")
+    whole = torch.full((rows + 2, (cols + 15) // 16 * 16 + 16), 77, dtype=torch.int8, device="cuda")
+    scales = torch.full((rows + 2,), -5.0, device="cuda")
+    fp4.fp4_quantize_int8(v, whole[1:rows + 1, :cols], scales[1:rows + 1])
+    check_quantized(v, whole[1:rows + 1, :cols], scales[1:rows + 1], (rows, cols))
+    whole[1:rows + 1, :cols] = 77              # nothing else was written
+    assert (whole == 77).all() and scales[0] == -5 and scales[-1] == -5
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_quantize_every_quotient_of_mantissas(dtype):
+    # rows: every mantissa of the maximum; columns: every mantissa of x at
+    # nine exponents.  Ties and their neighbours are all among them.
+    bits, one = (7, 0x3F80) if dtype == BF else (10, 0x3C00)
+    n = 1 << bits
+    amax = torch.arange(one, one + n, dtype=torch.int16).view(dtype)
+    xs = torch.cat([torch.arange(one - e * n, one - e * n + n, dtype=torch.int16).view(dtype) for e in range(9)])
+    x = xs[None, :].repeat(n, 1)
+    x = torch.where(x.float() <= amax[:, None].float(), x, -amax[:, None])
+    x = torch.cat([amax[:, None], x, torch.zeros(n, 7, dtype=dtype)], 1).cuda()
+    codes, scales = fp4.quantize_int8(x)
+    check_quantized(x, codes, scales)
+    assert (codes[:, 0] == 127).all()
+
+
+def test_quantize_extreme_rows():
+    # subnormal, smallest, largest and mixed magnitudes
+    tiny = torch.tensor([2.0 ** -133, 2.0 ** -126, 2.0 ** -118, 2.0 ** -100, 3.0 * 2.0 ** -132])
+    big = torch.tensor([3.3895314e38, 2.0 ** 127, 1.5 * 2.0 ** 120])
+    rows = [torch.linspace(-1, 1, 64) * v for v in list(tiny) + list(big)]
+    rows += [torch.cat([torch.full((32,), float(tiny[0])), torch.full((32,), float(big[0]))])]
+    x = torch.stack(rows).to(BF).cuda()
+    codes, scales = fp4.quantize_int8(x)
+    check_quantized(x, codes, scales, "bf16")
+    y = torch.stack([torch.linspace(-1, 1, 64) * v for v in (65504.0, 2.0 ** -24, 2.0 ** -14, 6e-8)]).to(HF).cuda()
+    check_quantized(y, *fp4.quantize_int8(y), what="fp16")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("cols", [40, 3001])
+def test_quantize_zero_and_non_finite_rows(dtype, cols):
+    x = torch.randn(6, cols, generator=torch.Generator().manual_seed(1)).to(dtype)
+    x[1] = 0
+    x[2, cols - 1] = float("inf")
+    x[3, 0] = float("-inf")
+    x[4, cols // 2] = float("nan")
+    x[5] = -0.0
+    x = torch.nn.functional.pad(x, (0, -cols % 8)).cuda()[:, :cols]
+    codes, scales = fp4.quantize_int8(x)
+    keep = [0, 1, 5]
+    check_quantized(x[keep], codes[keep], scales[keep])
+    assert torch.isnan(scales[2:5]).all() and (codes[2:5] == 0).all()
+    assert scales[1] == 1 and scales[5] == 1
+    w = torch.randint(-127, 128, (16, cols), dtype=torch.int8)
+    w = torch.nn.functional.pad(w, (0, -cols % 16)).cuda()[:, :cols]
+    for kernel in KERNELS:                     # such a token's outputs are NaN, the others' are not
+        d = fp4.gemm_int8(codes, scales, w, torch.ones(16, device="cuda"), kernel=kernel)
+        assert torch.isnan(d[2:5].float()).all() and torch.isfinite(d[[0, 1, 5]].float()).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("cols", [64, 1001, 5000])
+def test_quantize_gathers_rows(dtype, cols):
+    x = torch.randn(10, (cols + 7) // 8 * 8, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()[:, :cols]
+    index = torch.tensor([3, 3, 9, 0, 3, 5, 0, 9, 1, 2, 4, 6, 7, 8, 3, 3, 3], dtype=torch.int32, device="cuda")
+    codes, scales = fp4.quantize_int8(x, index)
+    check_quantized(x[index.long()], codes, scales)
+    index[::3] = torch.tensor([-1, 10, 2 ** 31 - 1, -2 ** 31, 11, -7], dtype=torch.int32, device="cuda")
+    codes, scales = fp4.quantize_int8(x, index)
+    assert (codes[::3] == 0).all() and (scales[::3] == 1).all()
+    kept = torch.ones(17, dtype=torch.bool)
+    kept[::3] = False
+    check_quantized(x[index[kept.cuda()].long()], codes[kept.cuda()], scales[kept.cuda()])
+
+
+# ---------------------------------------------------------------------------
+# Products
+# ---------------------------------------------------------------------------
+def random_codes(g, rows, cols, pad=16):
+    """Codes whose rows end inside 77s."""
+    w = torch.full((rows, (cols + 15) // 16 * 16 + pad), 77, dtype=torch.int8)
+    w[:, :cols] = torch.randint(-128, 128, (rows, cols), generator=g, dtype=torch.int8)
+    return w.cuda()[:, :cols]
+
+
+def check_product(d, a, sa, b, sb, bias, what=""):
+    p = (a.double() @ b.double().T) * sa.double()[:, None] * sb.double()[None, :]
+    y = p if bias is None else p + bias.double()
+    u = torch.finfo(d.dtype).eps / 2
+    e32 = 2.0 ** -24 * (3 * p.abs() + y.abs())
+    tol = u * y.abs() + (1 + u) * e32 + (2.0 ** -25 if d.dtype == HF else 0.0)
+    off = (d.double() - y).abs()
+    bad = torch.nonzero(~(off <= tol))
+    assert bad.numel() == 0, "%s: %d of %d outside, first %s: %r for %r" % (
+        what, len(bad), d.numel(), bad[0].tolist(), d[tuple(bad[0])].item(), y[tuple(bad[0])].item())
+
+
+def operands(M, N, K, seed, bias, experts=None):
+    g = torch.Generator().manual_seed(seed)
+    a, sa = random_codes(g, M, K), (torch.rand(M, generator=g) * 2e-3 + 1e-4).cuda()
+    n = N * (experts or 1)
+    b, sb = random_codes(g, n, K, pad=32), (torch.rand(n, generator=g) * 2e-3 + 1e-4).cuda()
+    c = torch.randn(n, generator=g).cuda() if bias else None
+    return a, sa, b, sb, c
+
+
+DENSE = [(1, 1, 1), (1, 8, 16), (3, 7, 5), (2, 130, 31), (16, 128, 128), (17, 130, 129), (33, 257, 300), (64, 200, 1024),
+         (65, 264, 640), (129, 513, 1000), (256, 256, 128), (257, 520, 2051), (700, 1030, 384), (1, 4096, 4096),
+         (5, 1000, 1151), (16, 4104, 1024), (100, 2048, 2048)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("MNK", DENSE)
+def test_dense_shapes(dtype, MNK):
+    M, N, K = MNK
+    a, sa, b, sb, bias = operands(M, N, K, 7 + M, bias=M % 2 == 1)
+    seen = []
+    for kernel in KERNELS + [fp4.GEMM_AUTO | fp4.GEMM_B_STATIC, fp4.GEMM_DECODE | fp4.GEMM_B_STATIC]:
+        whole = torch.full((M + 2, (N + 7) // 8 * 8 + 8), 3.0, dtype=dtype, device="cuda")
+        d = whole[1:M + 1, :N]
+        fp4.fp4_gemm_int8(a, sa, b, sb, d, bias, kernel)
+        check_product(d, a, sa, b, sb, bias, (MNK, kernel))
+        seen.append(d.clone())
+        whole[1:M + 1, :N] = 3.0
+        assert (whole == 3.0).all(), "wrote outside D"
+    assert all(torch.equal(s, seen[0]) for s in seen)
+
+
+# several tiles a CTA pair at either tile width, the grouped raster (A above
+# 64 MB), all token tiles of the other kernel, large M on it
+@pytest.mark.parametrize("MNK,kernel", [((2048, 5120, 512), fp4.GEMM_PREFILL), ((1024, 4600, 256), fp4.GEMM_PREFILL),
+                                        ((8450, 300, 8192), fp4.GEMM_PREFILL), ((600, 1000, 512), fp4.GEMM_DECODE),
+                                        ((16, 28672, 1024), fp4.GEMM_DECODE), ((128, 19000, 500), fp4.GEMM_DECODE),
+                                        ((300, 40000, 256), fp4.GEMM_AUTO)])
+def test_dense_many_tiles(MNK, kernel):
+    M, N, K = MNK
+    a, sa, b, sb, bias = operands(M, N, K, 3, bias=True)
+    d = fp4.gemm_int8(a, sa, b, sb, bias, kernel=kernel)
+    check_product(d, a, sa, b, sb, bias, MNK)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_dense_largest_sums(kernel):
+    K = 131071                                  # 128 * 128 * K = 2^31 - 16384
+    a = torch.full((2, K + 1), -128, dtype=torch.int8, device="cuda")[:, :K]
+    b = torch.full((9, K + 1), -128, dtype=torch.int8, device="cuda")[:, :K]
+    b[1] = 127
+    sa, sb = torch.full((2,), 2.0 ** -20, device="cuda"), torch.ones(9, device="cuda")
+    d = fp4.gemm_int8(a, sa, b, sb, kernel=kernel)
+    y = torch.full((2, 9), 16384.0 * K * 2.0 ** -20, dtype=torch.float64, device="cuda")
+    y[:, 1] = -128.0 * 127 * K * 2.0 ** -20
+    assert ((d.double() - y).abs() <= (2.0 ** -8 + 2.0 ** -22) * y.abs()).all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("bias", [False, True])
+def test_dense_empty_sums(kernel, bias):
+    a, b = torch.empty(5, 0, dtype=torch.int8, device="cuda"), torch.empty(9, 0, dtype=torch.int8, device="cuda")
+    c = torch.arange(9, dtype=torch.float32, device="cuda") if bias else None
+    d = fp4.gemm_int8(a, torch.ones(5, device="cuda"), b, torch.ones(9, device="cuda"), c, kernel=kernel)
+    assert torch.equal(d.float(), c.expand(5, 9) if bias else torch.zeros(5, 9, device="cuda"))
+    for M, N in ((0, 9), (5, 0), (0, 0)):
+        fp4.gemm_int8(torch.zeros(M, 16, dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda"),
+                      torch.zeros(N, 16, dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda"), kernel=kernel)
+
+
+# ---------------------------------------------------------------------------
+# By expert
+# ---------------------------------------------------------------------------
+def check_grouped(offsets, T, N, K, dtype, kernel, bias, seed=5, static=False):
+    E = len(offsets) - 1
+    a, sa, b, sb, c = operands(T, N, K, seed, bias, experts=E)
+    b, sb, c = b.unflatten(0, (E, N)), sb.view(E, N), c.view(E, N) if bias else None
+    whole = torch.full((T + 2, (N + 7) // 8 * 8 + 8), 3.0, dtype=dtype, device="cuda")
+    d = whole[1:T + 1, :N]
+    fp4.fp4_gemm_int8_grouped(a, sa, b, sb, torch.tensor(offsets, dtype=torch.int32, device="cuda"), d, c,
+                              kernel | (fp4.GEMM_B_STATIC if static else 0))
+    for e, (lo, hi) in enumerate(bounds_wanted(offsets, T)):
+        if lo < hi:
+            check_product(d[lo:hi], a[lo:hi], sa[lo:hi], b[e], sb[e], c[e] if bias else None, (e, lo, hi, kernel))
+            d[lo:hi] = 3.0
+    assert (whole == 3.0).all(), "wrote outside the groups"
+
+
+def ends(*counts, first=0):
+    return [first] + (first + np.cumsum(counts)).tolist()
+
+
+GROUPS = [
+    (ends(16), 16, 128, 128), (ends(0, 0, 1, 0), 1, 40, 64), (ends(0), 4, 40, 64),
+    (ends(3, 0, 20, 1, 0, 9), 40, 264, 300),                          # rows behind the last group
+    (ends(5, 1, 2, first=7), 20, 136, 1000),                          # rows before the first
+    (ends(255, 0, 256, 257, 1, 31), 800, 520, 257),
+    (ends(300, 2, 140, 0, 0, 33, 65, 1), 541, 1000, 512),
+    (ends(*([1] * 33)), 33, 72, 96), (ends(*([0, 7] * 40)), 280, 130, 160),
+    (ends(*([2, 0, 1, 5] * 128)), 1024, 24, 48),                      # 512 experts
+    (ends(900, 1500, 20), 2420, 5003, 130),                           # several tiles a CTA pair
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("case", range(len(GROUPS)))
+def test_grouped(case, kernel, dtype):
+    offsets, T, N, K = GROUPS[case]
+    check_grouped(offsets, T, N, K, dtype, kernel, bias=case % 2 == 0, static=case % 3 == 0)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("offsets", [[0, 30, 10, 50], [-5, 20, 400, 100], [90, 40, 40, 100], [2 ** 31 - 1, 0, 5, -2 ** 31],
+                                     [0, 0, 0, 0], [100, 100, 100, 100], [-1, -2 ** 31, 7, 2 ** 31 - 1]])
+def test_grouped_offsets_out_of_order_or_range(kernel, offsets):
+    check_grouped(offsets, 100, 72, 160, BF, kernel, bias=True)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_grouped_weights_with_gaps_between_experts(kernel):
+    g = torch.Generator().manual_seed(9)
+    E, N, K, T = 3, 50, 70, 30
+    store = torch.randint(-128, 128, (E, N + 5, 96), generator=g, dtype=torch.int8).cuda()
+    b = store[:, 2:2 + N, 16:16 + K]
+    a, sa, sb = random_codes(g, T, K), torch.rand(T, generator=g).cuda(), torch.rand(E, N, generator=g).cuda()
+    d = fp4.gemm_int8_grouped(a, sa, b, sb, torch.tensor([0, 11, 11, 30], dtype=torch.int32, device="cuda"), kernel=kernel)
+    check_product(d[:11], a[:11], sa[:11], b[0], sb[0], None)
+    check_product(d[11:], a[11:], sa[11:], b[2], sb[2], None)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_grouped_empty_sums_and_no_rows(kernel):
+    b = torch.empty(2, 9, 0, dtype=torch.int8, device="cuda")
+    c = torch.arange(18, dtype=torch.float32, device="cuda").view(2, 9)
+    off = torch.tensor([1, 3, 4], dtype=torch.int32, device="cuda")
+    d = torch.full((6, 16), 7.0, dtype=BF, device="cuda")
+    fp4.fp4_gemm_int8_grouped(torch.empty(6, 0, dtype=torch.int8, device="cuda"), torch.ones(6, device="cuda"), b,
+                              torch.ones(2, 9, device="cuda"), off, d[:, :9], c, kernel)
+    want = torch.full((6, 16), 7.0, device="cuda")
+    want[1:3, :9], want[3, :9] = c[0], c[1]
+    assert torch.equal(d.float(), want)
+    fp4.gemm_int8_grouped(torch.empty(0, 16, dtype=torch.int8, device="cuda"), torch.ones(0, device="cuda"),
+                          torch.zeros(2, 9, 16, dtype=torch.int8, device="cuda"), torch.ones(2, 9, device="cuda"), off,
+                          kernel=kernel)
+
+
+# ---------------------------------------------------------------------------
+# Together, on streams and in graphs
+# ---------------------------------------------------------------------------
+def weights(g, experts, N, K):
+    w = (torch.randn(experts * N, K, generator=g) * 0.02).to(BF).cuda()
+    codes, scales = fp4.quantize_int8(w)
+    check_quantized(w, codes, scales)
+    return codes.unflatten(0, (experts, N)), scales.view(experts, N)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("M", [1, 9, 40, 300])
+def test_linear(dtype, M):
+    g = torch.Generator().manual_seed(11)
+    N, K = 392, 840
+    w, sw = weights(g, 1, N, K)
+    x, bias = torch.randn(M, K, generator=g).to(dtype).cuda(), torch.randn(N, generator=g).cuda()
+    y = fp4.linear_int8(x, w[0], sw[0], bias)
+    codes, scales = fp4.quantize_int8(x)
+    check_quantized(x, codes, scales)
+    check_product(y, codes, scales, w[0], sw[0], bias)
+    # against the product that was never quantized: each code is off by at most half a step of its row
+    exact = x.double() @ (w[0].double() * sw[0].double()[:, None]).T + bias.double()
+    step = 0.5 * scales.double()[:, None] * (w[0].double().abs() * sw[0].double()[:, None]).sum(1)[None, :]
+    u = torch.finfo(dtype).eps / 2
+    assert ((y.double() - exact).abs() <= step * 1.01 + 1.01 * u * (exact.abs() + step) + 2.0 ** -20).all()
+
+
+def moe(x, index, off, up, sup, down, sdown):
+    a, sa = fp4.quantize_int8(x, index)
+    h = fp4.gemm_int8_grouped(a, sa, up, sup, off, kernel=fp4.GEMM_AUTO | fp4.GEMM_B_STATIC)
+    b, sb = fp4.quantize_int8(h)
+    return a, sa, h, b, sb, fp4.gemm_int8_grouped(b, sb, down, sdown, off, kernel=fp4.GEMM_AUTO | fp4.GEMM_B_STATIC)
+
+
+def check_moe(x, index, off, up, sup, down, sdown, got):
+    a, sa, h, b, sb, y = got
+    check_quantized(x[index.long()], a, sa)
+    check_quantized(h, b, sb)
+    o = off.tolist()
+    for e in range(len(o) - 1):
+        s = slice(o[e], o[e + 1])
+        if o[e] < o[e + 1]:
+            check_product(h[s], a[s], sa[s], up[e], sup[e], None)
+            check_product(y[s], b[s], sb[s], down[e], sdown[e], None)
+
+
+def routing(g, tokens, experts):
+    """Two experts a token: source rows in the experts' order, and the group bounds."""
+    picks = torch.stack([torch.randperm(experts, generator=g)[:2] for _ in range(tokens)]).flatten()
+    order = torch.argsort(picks, stable=True)
+    counts = torch.bincount(picks, minlength=experts)
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+    return (order // 2).to(torch.int32).cuda(), off.to(torch.int32).cuda()
+
+
+@pytest.mark.parametrize("tokens", [1, 30, 700])
+def test_expert_layer_and_its_graph(tokens):
+    g = torch.Generator().manual_seed(12)
+    E, H, F = 6, 256, 328
+    up, sup = weights(g, E, F, H)
+    down, sdown = weights(g, E, H, F)
+    x = torch.randn(tokens, H, generator=g).to(BF).cuda()
+    index, off = routing(g, tokens, E)
+    check_moe(x, index, off, up, sup, down, sdown, moe(x, index, off, up, sup, down, sdown))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        moe(x, index, off, up, sup, down, sdown)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = moe(x, index, off, up, sup, down, sdown)
+    for _ in range(3):                          # other tokens, other routing, the same graph
+        x.copy_(torch.randn(tokens, H, generator=g).to(BF))
+        i2, o2 = routing(g, tokens, E)
+        index.copy_(i2)
+        off.copy_(o2)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_moe(x, index, off, up, sup, down, sdown, got)
+
+
+def test_two_streams_at_once():
+    g = torch.Generator().manual_seed(13)
+    runs = []
+    for i, (M, N, K) in enumerate([(16, 6000, 2048), (16, 6000, 2048), (600, 1500, 512), (600, 1500, 512)]):
+        a, sa, b, sb, _ = operands(M, N, K, 20 + i, False)
+        runs.append((a, sa, b, sb, torch.empty(M, (N + 7) // 8 * 8, dtype=BF, device="cuda")[:, :N], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, sa, b, sb, d, s in runs:
+            fp4.fp4_gemm_int8(a, sa, b, sb, d, stream=s)
+    torch.cuda.synchronize()
+    for a, sa, b, sb, d, _ in runs:
+        check_product(d, a, sa, b, sb, None)
+
+
+def test_chain_without_waits():
+    # each product's output is the next one's input, nothing waits in between
+    g = torch.Generator().manual_seed(14)
+    w, sw = weights(g, 1, 512, 512)
+    x = torch.randn(20, 512, generator=g).to(BF).cuda()
+    want = x
+    for _ in range(12):
+        want = fp4.linear_int8(want, w[0], sw[0])
+        want = (want.float() * 2.2).to(BF)
+        torch.cuda.synchronize()
+    for _ in range(5):
+        y = x
+        for _ in range(12):
+            y = fp4.linear_int8(y, w[0], sw[0])
+            y = (y.float() * 2.2).to(BF)
+        assert torch.equal(y, want)
+
+
+def test_bound_calls():
+    a, sa, b, sb, bias = operands(20, 100, 200, 15, True)
+    d = torch.zeros(20, 104, dtype=BF, device="cuda")[:, :100]
+    fp4.bind_gemm_int8(a, sa, b, sb, d, bias)()
+    check_product(d, a, sa, b, sb, bias)
+    d.zero_()
+    off = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    fp4.bind_gemm_int8_grouped(a, sa, b[None], sb[None], off, d, bias[None])()
+    check_product(d, a, sa, b, sb, bias)
+    x = torch.randn(4, 96, device="cuda").to(BF)
+    codes, scales = torch.empty(4, 96, dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda")
+    fp4.bind_quantize_int8(x, codes, scales)()
+    check_quantized(x, codes, scales)
+
+
+def test_binding_refusals():
+    a, sa, b, sb, bias = operands(4, 16, 64, 16, True)
+    d = torch.zeros(4, 16, dtype=BF, device="cuda")
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    x = torch.zeros(4, 64, dtype=BF, device="cuda")
+    bad = [
+        lambda: fp4.fp4_gemm_int8(a, sa, b[:, :32], sb, d), lambda: fp4.fp4_gemm_int8(a.short(), sa, b, sb, d),
+        lambda: fp4.fp4_gemm_int8(a, sa, b, sb, d.float()), lambda: fp4.fp4_gemm_int8(a, sa.double(), b, sb, d),
+        lambda: fp4.fp4_gemm_int8(a, sa[:3], b, sb, d), lambda: fp4.fp4_gemm_int8(a, sa, b, sb, d, bias[:8]),
+        lambda: fp4.fp4_gemm_int8(a, sa, b, sb, d.T), lambda: fp4.fp4_gemm_int8(a.cpu(), sa, b, sb, d),
+        lambda: fp4.fp4_gemm_int8(a, sa, b, sb, torch.zeros(4, 20, dtype=BF, device="cuda")[:, :16]),   # ldd % 8
+        lambda: fp4.fp4_gemm_int8_grouped(a, sa, b, sb, off, d),
+        lambda: fp4.fp4_gemm_int8_grouped(a, sa, b[None], sb[None], off.long(), d),
+        lambda: fp4.fp4_gemm_int8_grouped(a, sa, b[None], sb[None], off[:1], d),
+        lambda: fp4.fp4_gemm_int8_grouped(a, sa, b[None].expand(2, 16, 64), sb[None].repeat(2, 1), off[[0, 0, 1]], d),
+        lambda: fp4.quantize_int8(x.float()), lambda: fp4.quantize_int8(x, off.long()),
+        lambda: fp4.fp4_quantize_int8(x, torch.zeros(4, 64, dtype=torch.uint8, device="cuda"), sa),
+        lambda: fp4.fp4_quantize_int8(x, torch.zeros(5, 64, dtype=torch.int8, device="cuda"), torch.zeros(5, device="cuda")),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((TypeError, ValueError, fp4.Fp4Error)):
+            call()
+            pytest.fail("call %d was accepted" % i)
+    assert (d == 0).all()
