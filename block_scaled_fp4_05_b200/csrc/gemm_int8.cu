@@ -199,11 +199,54 @@ struct SwapCfg {
     static constexpr int STAGE_BYTES = I8_TILE + NT * I8_BK;
     static constexpr int OFF_T = I8_TILE;
     static constexpr int OFF_BARS = STAGES * STAGE_BYTES;
-    static constexpr int SMEM = OFF_BARS + 256 + 1024;
+    static constexpr int OFF_SCALE = OFF_BARS + 256;   // sA of the tokens, sB and bias of the channels
+    static constexpr int SMEM = OFF_SCALE + (NT + 2 * I8_BM) * 4 + 1024;
     static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
     static_assert(NT * I8_BM * 4 <= OFF_BARS, "the sums reuse the stages' memory");
     static_assert((2 * STAGES + 2) * 8 + 32 <= 256, "barrier area");
 };
+
+// Adds the S CTAs' sums for this CTA's channels, scales and stores.  A thread
+// has four channels (the same ones for all its tokens) and every
+// (kSwapThreads / pieces)-th token.
+template <int S, bool HALF>
+__device__ __forceinline__ void swap_finish(const I8Params& p, uint32_t sums, const float* sas, const float* sbs,
+                                            int rank, int row0, int ntok, int n0)
+{
+    constexpr int PIECES = I8_BM / 4 / S;
+    static_assert(kSwapThreads % PIECES == 0, "a thread keeps its channels");
+    const int ch = (rank * PIECES + threadIdx.x % PIECES) * 4;   // within the tile
+    const int n = n0 + ch;
+    if (n >= p.N) return;
+    const float4 sb = *reinterpret_cast<const float4*>(sbs + ch);
+    const float4 bias = *reinterpret_cast<const float4*>(sbs + I8_BM + ch);
+    uint32_t from[S];
+#pragma unroll
+    for (int r = 0; r < S; ++r) from[r] = map_to_rank(sums + ch * 4u, r);
+    for (int tok = threadIdx.x / PIECES; tok < ntok; tok += kSwapThreads / PIECES) {
+        int4 v[S];
+#pragma unroll
+        for (int r = 0; r < S; ++r) v[r] = ld_cluster_v4(from[r] + (uint32_t)tok * (I8_BM * 4));
+#pragma unroll
+        for (int r = 1; r < S; ++r) {
+            v[0].x += v[r].x;
+            v[0].y += v[r].y;
+            v[0].z += v[r].z;
+            v[0].w += v[r].w;
+        }
+        const float sa = sas[tok];
+        const uint32_t lo = pack16<HALF>(scaled(v[0].x, sa, sb.x, bias.x), scaled(v[0].y, sa, sb.y, bias.y));
+        const uint32_t hi = pack16<HALF>(scaled(v[0].z, sa, sb.z, bias.z), scaled(v[0].w, sa, sb.w, bias.w));
+        uint16_t* d = p.D + (int64_t)(row0 + tok) * p.ldd + n;
+        if (n + 4 <= p.N) {
+            *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+        } else {
+            d[0] = (uint16_t)lo;
+            if (n + 1 < p.N) d[1] = (uint16_t)(lo >> 16);
+            if (n + 2 < p.N) d[2] = (uint16_t)hi;
+        }
+    }
+}
 
 template <int NT, bool HALF>
 __global__ void __launch_bounds__(kSwapThreads)
@@ -220,17 +263,24 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     int* shared_word = reinterpret_cast<int*>(bars + 2 * STAGES + 1);
     // [0] tensor-memory base, [1] abort, [2..5] expert, first row, rows, tile within the expert
     volatile int* abort_flag = shared_word + 1;
+    float* sas = reinterpret_cast<float*>(smem + C::OFF_SCALE);   // [NT]
+    float* sbs = sas + NT;                                        // [128], then the bias [128]
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     uint32_t split;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
     const int rank = (int)cluster_rank();
+    const int kb = (int)((int64_t)p.ks_total * rank / (int)split);
+    const int ke = (int)((int64_t)p.ks_total * (rank + 1) / (int)split);
     const uint32_t smem0 = smem_u32(smem);
     const uint32_t bar0 = smem_u32(bars);
     auto FULL = [&](int s) { return bar0 + 8u * s; };
     auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
     const uint32_t acc_full = bar0 + 8u * (2 * STAGES);
+    // Weight tiles requested before the dependency wait (static weights of a
+    // dense product): those of the first stages, their token tiles follow.
+    const int pre = !p.offsets && p.b_static ? min(STAGES, ke - kb) : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -241,12 +291,21 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (pre > 0) {
+            const int mt = (p.M + NT - 1) / NT;
+            const int tn = (int)(blockIdx.x / split) / mt;
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(FULL(i), C::STAGE_BYTES);
+                tma_load_3d(&tmW, FULL(i), smem0 + i * C::STAGE_BYTES, (kb + i) * I8_BK, tn * I8_BM, 0);
+            }
+        }
     }
     // The tile: cluster c takes the c-th of the list (expert, channel tile,
     // token tile), token tiles fastest, so that the CTAs that share weights
     // run next to each other.
     if (p.offsets) {
         if (warp == 0) {
+            __syncwarp();
             pdl_wait();
             const int64_t c = blockIdx.x / split;
             int64_t seen = 0;   // tiles of the experts before e0
@@ -269,15 +328,9 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             }
             if (!found && lane == 0) shared_word[2] = -1;
         }
-    } else if (threadIdx.x == 0) {
-        shared_word[2] = 0;
-        shared_word[3] = 0;
-        shared_word[4] = p.M;
-        shared_word[5] = (int)(blockIdx.x / split);
+        __syncthreads();
+        if (shared_word[2] < 0) return;   // no such tile: the whole cluster leaves
     }
-    __syncthreads();
-    const int expert = shared_word[2];
-    if (expert < 0) return;   // no such tile: the whole cluster leaves
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(shared_word)),
@@ -285,30 +338,26 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const int rows = shared_word[4];
-    const int mt = (rows + NT - 1) / NT;
-    const int tm = shared_word[5] % mt, tn = shared_word[5] / mt;
-    const int row0 = shared_word[3] + tm * NT;        // first token
-    const int ntok = min(NT, rows - tm * NT);
-    const int kb = (int)((int64_t)p.ks_total * rank / (int)split);
-    const int ke = (int)((int64_t)p.ks_total * (rank + 1) / (int)split);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = (uint32_t)shared_word[0];
+    int expert = 0, first = 0, rows = p.M, tile = (int)(blockIdx.x / split);
+    if (p.offsets) {
+        expert = shared_word[2];
+        first = shared_word[3];
+        rows = shared_word[4];
+        tile = shared_word[5];
+    }
+    const int mt = (rows + NT - 1) / NT;
+    const int tm = tile % mt, tn = tile / mt;
+    const int row0 = first + tm * NT;        // first token
+    const int ntok = min(NT, rows - tm * NT);
 
     if (warp == 0) {
         if (lane == 0 && kb < ke) {
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmX)) : "memory");
-            // Static weights: the first stages' weight tiles are requested
-            // before the dependency wait, their token tiles after it.
-            int pre = 0;
-            if (!p.offsets && p.b_static)
-                for (; pre < STAGES && kb + pre < ke; ++pre) {
-                    mbar_arrive_expect_tx(FULL(pre), C::STAGE_BYTES);
-                    tma_load_3d(&tmW, FULL(pre), smem0 + pre * C::STAGE_BYTES, (kb + pre) * I8_BK, tn * I8_BM, expert);
-                }
+            pdl_trigger();
             pdl_wait();
             int stage = 0;
             uint32_t phase = 0;
@@ -329,7 +378,6 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                     phase ^= 1u;
                 }
             }
-            pdl_trigger();
             if (!ok || *abort_flag) spin_ns(200000);   // loads in flight land before the memory is used again
         }
         __syncwarp();
@@ -358,7 +406,13 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         }
         __syncwarp();
     } else {
-        pdl_wait();   // the scales and D are touched below
+        pdl_wait();
+        const int i = threadIdx.x - 64;
+        const int64_t chan = (int64_t)expert * p.N + tn * I8_BM + i;
+        const bool in = tn * I8_BM + i < p.N;
+        if (i < ntok) sas[i] = __ldcg(p.sa + row0 + i);
+        sbs[i] = in ? __ldcg(p.sb + chan) : 0.0f;
+        sbs[I8_BM + i] = in && p.bias ? __ldcg(p.bias + chan) : 0.0f;
         const int q = warp & 3;   // tensor-memory lane quadrant: channels [32 q, 32 q + 32)
         const uint32_t dst = smem0 + (uint32_t)(q * 32 + lane) * 4u;
         const bool have = kb < ke && warp_wait(acc_full, 0, abort_flag, ERR_ACC_FULL);
@@ -381,7 +435,7 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (uint32_t)(c + i) * (I8_BM * 4)), "r"(r[i]) : "memory");
         }
     }
-    if (warp < 2) pdl_wait();   // these warps' threads read scales and write D below as well
+    if (warp < 2) pdl_wait();   // these warps write D below as well
     tc_fence_before();
     __syncwarp();
     if (split > 1)
@@ -392,46 +446,18 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS)
                      : "memory");
-
-    // This CTA's channels: [128 rank / S, 128 (rank + 1) / S) of the tile, four a thread.
-    const int pieces = I8_BM / 4 / (int)split;
-    const int64_t chan_base = (int64_t)expert * p.N;
-    for (int i = threadIdx.x; i < ntok * pieces; i += kSwapThreads) {
-        const int tok = i / pieces;
-        const int ch = (rank * pieces + i % pieces) * 4;   // within the tile
-        const int n = tn * I8_BM + ch;
-        if (n >= p.N) continue;
-        const uint32_t at = smem0 + (uint32_t)(tok * I8_BM + ch) * 4u;
-        int4 sum = make_int4(0, 0, 0, 0);
-        for (uint32_t r = 0; r < split; ++r) {
-            const int4 v = ld_cluster_v4(map_to_rank(at, r));
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
-        }
-        const int64_t row = (int64_t)row0 + tok;
-        const float sa = __ldcg(p.sa + row);
-        const int acc[4] = {sum.x, sum.y, sum.z, sum.w};
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = n + j < p.N;
-            const float sb = in ? __ldcg(p.sb + chan_base + n + j) : 0.0f;
-            const float bias = in && p.bias ? __ldcg(p.bias + chan_base + n + j) : 0.0f;
-            v[j] = scaled(acc[j], sa, sb, bias);
-        }
-        const uint32_t lo = pack16<HALF>(v[0], v[1]), hi = pack16<HALF>(v[2], v[3]);
-        uint16_t* d = p.D + row * p.ldd + n;
-        if (n + 4 <= p.N) {
-            *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
-        } else {
-            d[0] = (uint16_t)lo;
-            if (n + 1 < p.N) d[1] = (uint16_t)(lo >> 16);
-            if (n + 2 < p.N) d[2] = (uint16_t)hi;
-        }
+    if (split == 1)
+        swap_finish<1, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+    else if (split == 2)
+        swap_finish<2, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+    else if (split == 4)
+        swap_finish<4, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+    else
+        swap_finish<8, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+    if (split > 1) {
+        __syncwarp();
+        cluster_sync();   // no CTA leaves while another reads its sums
     }
-    if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums
 }
 
 // ------------------------------------------------------------------------

@@ -15,7 +15,7 @@
 // t + e r differs from the quotient by less than 2^-44 of it, so a quotient
 // that FP32 holds (every tie does) comes out exactly.  Adding 1.5 * 2^23 rounds
 // q to an integer, halves to even, and leaves its two's complement in the low
-// byte.  Seven operations an element instead of a division's dozens.
+// byte.  Two elements go through these steps in one instruction each.
 //
 // Bound by HBM: 2 bytes read and 1 written an element.  A row stays in the
 // registers of its threads between the maximum and the codes, so it is read
@@ -80,20 +80,47 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits)
     return s;
 }
 
-// The code of x in the low byte of the result (higher bytes: garbage).
-__device__ __forceinline__ uint32_t code(float x, const RowScale& s)
+// Two FP32 operations in one instruction (each rounded as its scalar form).
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
 {
-    const float a = __fmul_rn(x, s.c);
-    const float t = __fmul_rn(a, s.r);
-    const float q = __fmaf_rn(__fmaf_rn(-t, s.m, a), s.r, t);
-    return __float_as_uint(__fadd_rn(q, 12582912.0f));
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The codes of two elements in the low bytes of the halves (other bytes: garbage).
+__device__ __forceinline__ uint64_t code2(uint64_t x, uint64_t c, uint64_t neg_m, uint64_t r)
+{
+    const uint64_t a = mul2(x, c);
+    const uint64_t t = mul2(a, r);
+    const uint64_t q = fma2(fma2(t, neg_m, a), r, t);
+    return add2(q, pair(12582912.0f, 12582912.0f));
 }
 
 template <bool HALF>
 __device__ __forceinline__ uint2 codes8(uint4 v, const RowScale& s, bool finite)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t b[8];
+    const uint64_t c = pair(s.c, s.c), neg_m = pair(-s.m, -s.m), r = pair(s.r, s.r);
+    uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float lo, hi;
@@ -105,12 +132,11 @@ __device__ __forceinline__ uint2 codes8(uint4 v, const RowScale& s, bool finite)
             lo = __uint_as_float(w[i] << 16);
             hi = __uint_as_float(w[i] & 0xFFFF0000u);
         }
-        b[2 * i] = code(lo, s);
-        b[2 * i + 1] = code(hi, s);
+        const uint64_t q = code2(pair(lo, hi), c, neg_m, r);
+        b[i] = __byte_perm((uint32_t)q, (uint32_t)(q >> 32), 0x0040);
     }
     if (!finite) return make_uint2(0u, 0u);
-    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
-                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
 }
 
 // Elements [k, k + 8) of a row of `cols`; nothing behind the row is read.
@@ -150,18 +176,21 @@ struct QuantArgs {
 template <bool HALF, int TPR, int CH, int THREADS>
 __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const QuantArgs p)
 {
+    // The next kernel may start its set-up; this one starts before the one
+    // before it has ended (0.5 us a launch) and touches nothing until then.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int ROWS = THREADS / TPR;
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-    if (ROWS > 1 && row >= p.rows) return;   // whole warps
+    const bool have = ROWS == 1 || row < p.rows;   // the last block's rows may end before it
     int64_t src = row;
-    bool inside = true;
-    if (p.index) {
+    bool inside = have;
+    if (p.index && have) {
         src = __ldg(p.index + row);
         inside = src >= 0 && src < p.rows_in;   // an index outside gives a row of zeros
-        if (!inside) src = 0;
     }
+    if (!inside) src = 0;
     const uint16_t* x = p.x + src * p.ld;
     const int64_t cols = inside ? p.cols : 0;
     uint4 v[CH > 0 ? CH : 1];
@@ -179,12 +208,13 @@ __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const QuantArgs 
     }
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
     if (TPR > 32) {
-        __shared__ uint32_t part[TPR / 32];
-        if ((t & 31) == 0) part[t >> 5] = amax;
+        __shared__ uint32_t part[ROWS][TPR / 32];
+        if ((t & 31) == 0) part[threadIdx.x / TPR][t >> 5] = amax;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) amax = max(amax, part[i]);
+        for (int i = 0; i < TPR / 32; ++i) amax = max(amax, part[threadIdx.x / TPR][i]);
     }
+    if (!have) return;
     const RowScale s = row_scale<HALF>(amax);
     const bool finite = amax < (HALF ? 0x7C00u : 0x7F80u);
     if (t == 0) p.scales[row] = s.scale;
@@ -206,19 +236,28 @@ template <bool HALF, int TPR, int CH, int THREADS>
 cudaError_t launch(const QuantArgs& p, cudaStream_t s)
 {
     constexpr int ROWS = THREADS / TPR;
-    quantize_int8_kernel<HALF, TPR, CH, THREADS><<<(unsigned)((p.rows + ROWS - 1) / ROWS), THREADS, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.rows + ROWS - 1) / ROWS), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, quantize_int8_kernel<HALF, TPR, CH, THREADS>, p);
 }
 
 template <bool HALF>
 cudaError_t dispatch(const QuantArgs& p, cudaStream_t s)
 {
-    if (p.cols <= 256) return launch<HALF, 32, 1, 256>(p, s);
-    if (p.cols <= 512) return launch<HALF, 32, 2, 256>(p, s);
-    if (p.cols <= 1024) return launch<HALF, 32, 4, 256>(p, s);
-    if (p.cols <= 2048) return launch<HALF, 32, 8, 256>(p, s);
-    if (p.cols <= 4096) return launch<HALF, 256, 2, 256>(p, s);
-    if (p.cols <= 8192) return launch<HALF, 256, 4, 256>(p, s);
+    if (p.cols <= 256) return launch<HALF, 32, 1, 128>(p, s);
+    if (p.cols <= 512) return launch<HALF, 32, 2, 128>(p, s);
+    if (p.cols <= 1024) return launch<HALF, 32, 4, 128>(p, s);
+    if (p.cols <= 2048) return launch<HALF, 32, 8, 128>(p, s);
+    const bool many = p.rows > 1024;
+    if (p.cols <= 4096) return many ? launch<HALF, 128, 4, 128>(p, s) : launch<HALF, 256, 2, 256>(p, s);
+    if (p.cols <= 8192) return many ? launch<HALF, 128, 8, 128>(p, s) : launch<HALF, 256, 4, 256>(p, s);
     if (p.cols <= 16384) return launch<HALF, 256, 8, 256>(p, s);
     if (p.cols <= 32768) return launch<HALF, 512, 8, 512>(p, s);
     return launch<HALF, 512, 0, 512>(p, s);
