@@ -121,6 +121,14 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr)
     return v;
 }
 
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <bool HALF>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi)
 {
@@ -474,9 +482,8 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 //               for each stage, then opens the stage's named barrier
 //   warp 3      grouped: the tile list from the offsets
 //   warps 4-11  epilogue: two warps a tensor-memory lane quadrant, BN / 2
-//               columns each; scales, bias, 16 bits, 32 x 32 blocks through
-//               shared memory and TMA stores (row by row where a block
-//               reaches past its expert's last row)
+//               columns each; scales, bias, 16 bits, and from the registers
+//               to D in whole 32-byte sectors, a lane a row
 // Every wait is bounded; a CTA that gives up records it in the error word.
 // ------------------------------------------------------------------------
 constexpr int kI8PairThreads = 384;
@@ -488,10 +495,8 @@ struct I8PairCfg {
     static constexpr int STAGE_BYTES = I8_TILE + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 6 : 8;
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int EPI_BLOCK = 32 * 64;                 // 32 rows x 32 columns of 16 bits
     static constexpr int WARP_COLS = BN / 2;                  // columns of an epilogue warp
-    static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
-    static constexpr int OFF_SCALE = OFF_EPI + kI8EpiWarps * EPI_BLOCK;            // sB and bias of the warp's columns
+    static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;                         // sB and bias of a warp's columns
     static constexpr int OFF_LIST = OFF_SCALE + kI8EpiWarps * 2 * 128 * 4;         // experts' first tiles and bounds
     static constexpr int OFF_BARS = OFF_LIST + 2 * (kMaxExperts + 2) * 4;
     static constexpr int NBARS = 2 * STAGES + 5;
@@ -504,7 +509,7 @@ struct I8PairCfg {
 template <int BN, bool HALF, bool GROUPED>
 __global__ void __launch_bounds__(kI8PairThreads, 1)
 int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmD, const I8Params p)
+                 const I8Params p)
 {
     using C = I8PairCfg<BN>;
     constexpr int STAGES = C::STAGES;
@@ -617,24 +622,38 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if (lane == 0) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
-            int stage = 0;
+            int stage = 0, pre = 0;
             uint32_t phase = 0;
             bool ok = true;
+            if (!GROUPED && p.b_static && pair < tiles) {
+                // static weights: those of the first stages are requested
+                // before the dependency wait
+                const Place w = locate(pair);
+                for (; pre < STAGES && pre < p.ks_total; ++pre) {
+                    if (leader) mbar_arrive_expect_tx(FULL(pre), 2u * C::STAGE_BYTES);
+                    tma_load_3d_pair(&tmB, map_to_rank(FULL(pre), 0), smem0 + pre * C::STAGE_BYTES + I8_TILE,
+                                     pre * I8_BK, w.col + (int)rank * (BN / 2), w.e);
+                }
+            }
             pdl_wait();
             for (int t = pair; ok && t < tiles; t += npairs) {
                 const Place w = locate(t);
                 const int ya = w.row + (int)rank * I8_BM;
                 const int yb = w.col + (int)rank * (BN / 2);
                 for (int ks = 0; ks < p.ks_total; ++ks) {
-                    if (!wait_fast(EMPTY(stage), phase ^ 1u, abort_flag, ERR_EMPTY)) {
-                        ok = false;
-                        break;
-                    }
-                    if (leader) mbar_arrive_expect_tx(FULL(stage), 2u * C::STAGE_BYTES);
                     const uint32_t full = map_to_rank(FULL(stage), 0);
                     const uint32_t st = smem0 + stage * C::STAGE_BYTES;
+                    if (pre > 0) {
+                        --pre;   // this stage's B tile is on its way
+                    } else {
+                        if (!wait_fast(EMPTY(stage), phase ^ 1u, abort_flag, ERR_EMPTY)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) mbar_arrive_expect_tx(FULL(stage), 2u * C::STAGE_BYTES);
+                        tma_load_3d_pair(&tmB, full, st + I8_TILE, ks * I8_BK, yb, w.e);
+                    }
                     tma_load_3d_pair(&tmA, full, st, ks * I8_BK, ya, 0);
-                    tma_load_3d_pair(&tmB, full, st + I8_TILE, ks * I8_BK, yb, w.e);
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -705,9 +724,8 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int eb = warp - 4;
         float* sbs = reinterpret_cast<float*>(smem + C::OFF_SCALE) + eb * 256;
         float* bis = sbs + 128;
-        const uint32_t blk = smem0 + C::OFF_EPI + eb * C::EPI_BLOCK;
-        const uint32_t my_row = blk + lane * 64;
-        const int sw = (lane >> 1) & 3;
+        // whole 32-byte sectors where D's rows start on them
+        const bool wide = (reinterpret_cast<uintptr_t>(p.D) & 31) == 0 && (p.ldd & 15) == 0;
         pdl_wait();
         uint32_t acc_phase = 0;
         int buf = 0;
@@ -743,37 +761,23 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     packed[2 * i + 1] = pack16<HALF>(scaled((int)r[4 * i + 2], sa, s4.z, b4.z),
                                                      scaled((int)r[4 * i + 3], sa, s4.w, b4.w));
                 }
-                // A TMA store clips at the tensor's edge in whole 16 bytes, so
-                // the last columns of an N that is not a multiple of 8 are
-                // stored one by one; as are the rows of a block that holds
-                // the next expert's first ones too.
-                const bool whole = (!GROUPED || y0 + 32 <= w.row_end) && (x0 + 32 <= p.N || (p.N & 7) == 0);
-                if (whole) {
-                    // 64-byte rows, 16-byte piece j of row r at j ^ ((r >> 1) & 3): the 64-byte swizzle
-                    if (lane == 0) bulk_wait_read_all();   // the block's previous store has read it
-                    __syncwarp();
+                if (y0 + lane >= w.row_end) return;
+                uint16_t* d = p.D + (int64_t)(y0 + lane) * p.ldd + x0;
+                if (x0 + 32 <= p.N && wide) {
+                    st_global_v8(d, packed);
+                    st_global_v8(d + 16, packed + 8);
+                    return;
+                }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(my_row + ((j ^ sw) << 4)),
-                                     "r"(packed[4 * j]), "r"(packed[4 * j + 1]), "r"(packed[4 * j + 2]),
-                                     "r"(packed[4 * j + 3])
-                                     : "memory");
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) tma_store_2d(&tmD, blk, x0, y0);
-                } else if (y0 + lane < w.row_end) {
-                    uint16_t* d = p.D + (int64_t)(y0 + lane) * p.ldd + x0;
+                for (int j = 0; j < 4; ++j) {
+                    if (x0 + 8 * j + 8 <= p.N) {
+                        *reinterpret_cast<uint4*>(d + 8 * j) = make_uint4(packed[4 * j], packed[4 * j + 1],
+                                                                          packed[4 * j + 2], packed[4 * j + 3]);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (x0 + 8 * j + 8 <= p.N) {
-                            *reinterpret_cast<uint4*>(d + 8 * j) = make_uint4(packed[4 * j], packed[4 * j + 1],
-                                                                              packed[4 * j + 2], packed[4 * j + 3]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (x0 + 8 * j + i < p.N)
-                                    d[8 * j + i] = (uint16_t)(packed[4 * j + (i >> 1)] >> (16 * (i & 1)));
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            if (x0 + 8 * j + i < p.N)
+                                d[8 * j + i] = (uint16_t)(packed[4 * j + (i >> 1)] >> (16 * (i & 1)));
                     }
                 }
             };
@@ -803,8 +807,6 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             buf ^= 1;
             if (buf == 0) acc_phase ^= 1u;
         }
-        if (lane == 0) bulk_wait_all();   // every store of D has completed
-        __syncwarp();
     }
 
     tc_fence_before();
@@ -844,20 +846,6 @@ bool make_map_i8_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols
     cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// D [rows x cols] of 16 bits, stored in 32 x 32 boxes with the 64-byte swizzle.
-bool make_map_d16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld)
-{
-    auto enc = encoder();
-    if (!enc) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {32, 32};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -940,10 +928,9 @@ template <int BN, bool HALF, bool GROUPED>
 cudaError_t launch_pair(const Int8GemmArgs& a, int64_t tiles, int sm_count, cudaStream_t s)
 {
     using C = I8PairCfg<BN>;
-    CUtensorMap ta, tb, td;
+    CUtensorMap ta, tb;
     if (!make_map_i8(&ta, a.A, 1, a.M, a.K, a.lda, a.lda, I8_BM) ||
-        !make_map_i8(&tb, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, BN / 2) ||
-        !make_map_d16(&td, a.D, a.M, a.N, a.ldd)) {
+        !make_map_i8(&tb, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, BN / 2)) {
         set_last_error("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
         return cudaErrorInvalidValue;
     }
@@ -962,7 +949,7 @@ cudaError_t launch_pair(const Int8GemmArgs& a, int64_t tiles, int sm_count, cuda
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         launch_config(cfg, attr, 2u * (unsigned)(tiles < pairs ? tiles : pairs), kI8PairThreads, 2, C::SMEM, s);
-        e = cudaLaunchKernelEx(&cfg, kern, ta, tb, td, p);
+        e = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
     }
     if (e != cudaSuccess) set_last_error("INT8 GEMM launch (CTA pairs)", e);
     return e;
