@@ -52,7 +52,10 @@ struct I8Params {
     int32_t M, N;            // rows of A and D, output channels
     int32_t ks_total;        // stages of a tile (0: K = 0, the sums are zero)
     int32_t tiles_n;
-    int32_t raster_gm;       // pair kernel: M tiles per group of the tile order
+    // pair kernel: tile width and its stages, whether a partial last wave may
+    // be halved, M tiles per group of the tile order
+    int32_t bn, stages, halves;
+    int32_t raster_gm;
     int32_t E;               // experts (dense: 1)
     const int32_t* offsets;  // [E + 1] (dense: NULL, one group of all M rows)
     int32_t b_static;        // B is not written by the previous kernel
@@ -469,10 +472,11 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 }
 
 // ------------------------------------------------------------------------
-// Many tokens: a cluster of two CTAs computes a 256 x BN tile with pair MMAs
-// (M = 256, N = BN): each CTA stages its own 128 rows of A and half of the
-// tile's B rows.  Two accumulators in tensor memory, so that a tile's
-// epilogue runs beside the next tile's MMAs.
+// Many tokens: a cluster of two CTAs computes a 256 x bn tile with pair MMAs
+// (M = 256, N = bn, a multiple of 32 up to 256 that the host chooses): each
+// CTA stages its own 128 rows of A and half of the tile's B rows.  Two
+// accumulators in tensor memory, so that a tile's epilogue runs beside the
+// next tile's MMAs.
 //   warp 0      producer (both CTAs; loads complete on the leader's full[s])
 //   warp 1      MMA issue (leader): passes a stage's named barrier, issues
 //               four MMAs and the commit that releases the stage in both
@@ -481,62 +485,65 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 //   warp 2      gatekeeper (leader): waits for the accumulator's release and
 //               for each stage, then opens the stage's named barrier
 //   warp 3      grouped: the tile list from the offsets
-//   warps 4-11  epilogue: two warps a tensor-memory lane quadrant, BN / 2
-//               columns each; scales, bias, 16 bits, and from the registers
-//               to D in whole 32-byte sectors, a lane a row
+//   warps 4-11  epilogue: two warps a tensor-memory lane quadrant, 32 columns
+//               in turn; scales, bias, 16 bits, and from the registers to D
+//               in whole 32-byte sectors, a lane a row
 // Every wait is bounded; a CTA that gives up records it in the error word.
 // ------------------------------------------------------------------------
 constexpr int kI8PairThreads = 384;
 constexpr int kI8EpiWarps = 8;
+constexpr int kI8PairMaxStages = 12;
 
-template <int BN>
-struct I8PairCfg {
-    static constexpr int B_BYTES = BN / 2 * I8_BK;
-    static constexpr int STAGE_BYTES = I8_TILE + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 6 : 8;
-    static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int WARP_COLS = BN / 2;                  // columns of an epilogue warp
-    static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;                         // sB and bias of a warp's columns
+struct I8Pair {
+    static constexpr int OFF_SCALE = 0;                                            // sB and bias of a warp's columns
     static constexpr int OFF_LIST = OFF_SCALE + kI8EpiWarps * 2 * 128 * 4;         // experts' first tiles and bounds
     static constexpr int OFF_BARS = OFF_LIST + 2 * (kMaxExperts + 2) * 4;
-    static constexpr int NBARS = 2 * STAGES + 5;
-    static constexpr int SMEM = OFF_BARS + 256 + 1024;
+    static constexpr int NBARS = 2 * kI8PairMaxStages + 5;
+    static constexpr int FIXED = (OFF_BARS + 256 + 1023) / 1024 * 1024;            // what lies before the stages
+    static constexpr int SMEM = 232448;
+    static constexpr int STAGE_ROOM = SMEM - 1024 - FIXED;
     static_assert(NBARS * 8 + 8 <= 256, "barrier area");
     static_assert(OFF_BARS % 16 == 0, "barrier alignment");
-    static_assert(SMEM <= 232448, "shared memory per CTA");
+    static_assert(kI8PairMaxStages + 1 <= 16, "one named barrier per stage (ids from 1)");
+    __host__ __device__ static constexpr int stage_bytes(int bn) { return I8_TILE + bn / 2 * I8_BK; }
+    static constexpr int stages(int bn)
+    {
+        const int n = STAGE_ROOM / stage_bytes(bn);
+        return n < kI8PairMaxStages ? n : kI8PairMaxStages;
+    }
 };
 
-template <int BN, bool HALF, bool GROUPED>
+template <bool HALF, bool GROUPED>
 __global__ void __launch_bounds__(kI8PairThreads, 1)
 int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const I8Params p)
+                 const __grid_constant__ CUtensorMap tmBh, const I8Params p)
 {
-    using C = I8PairCfg<BN>;
-    constexpr int STAGES = C::STAGES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
-    // [0,S) full (leader), [S,2S) empty, [2S..2S+1] acc_full, [2S+2..2S+3] acc_empty (leader), [2S+4] drain
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBARS);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + I8Pair::OFF_BARS);
+    // [0,12) full (leader), [12,24) empty, [24..25] acc_full, [26..27] acc_empty (leader), [28] drain
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + I8Pair::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* list = reinterpret_cast<int*>(smem + C::OFF_LIST);   // [E + 1] first tile of each expert
-    int* bound = list + kMaxExperts + 2;                      // [E + 1] its first row
+    int* list = reinterpret_cast<int*>(smem + I8Pair::OFF_LIST);   // [E + 1] first tile of each expert
+    int* bound = list + kMaxExperts + 2;                           // [E + 1] its first row
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
-    const uint32_t smem0 = smem_u32(smem);
+    const int stages = p.stages;
+    const uint32_t stage_bytes = (uint32_t)I8Pair::stage_bytes(p.bn);
+    const uint32_t smem0 = smem_u32(smem) + I8Pair::FIXED;   // first stage
     const uint32_t bar0 = smem_u32(bars);
     auto FULL = [&](int s) { return bar0 + 8u * s; };
-    auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    auto ACC_FULL = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
-    auto ACC_EMPTY = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-    const uint32_t drain = bar0 + 8u * (2 * STAGES + 4);
+    auto EMPTY = [&](int s) { return bar0 + 8u * (kI8PairMaxStages + s); };
+    auto ACC_FULL = [&](int b) { return bar0 + 8u * (2 * kI8PairMaxStages + b); };
+    auto ACC_EMPTY = [&](int b) { return bar0 + 8u * (2 * kI8PairMaxStages + 2 + b); };
+    const uint32_t drain = bar0 + 8u * (2 * kI8PairMaxStages + 4);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(FULL(s), 1);
             mbar_init(EMPTY(s), 1);
         }
@@ -552,7 +559,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(tmem_slot)),
-                     "r"(C::TMEM_COLS)
+                     "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -583,15 +590,27 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int pair = blockIdx.x >> 1;
     const int npairs = gridDim.x >> 1;
     const int tiles = GROUPED ? list[p.E] : (p.M + 255) / 256 * p.tiles_n;
-    // Expert, first row and channel of tile t, and the end of the expert's
-    // rows.  Within an expert groups of raster_gm consecutive M tiles sweep
-    // the N tiles together (M fastest), so that a group's A rows stay in L2
-    // while B streams past them once.
+    // Work items: the tiles, dealt round-robin.  A last, partial wave whose
+    // halves fit on the pairs is computed as halves of bn / 2 columns.
+    const int rem = tiles % npairs;
+    const int split_from = p.halves && 2 * rem <= npairs ? tiles - rem : tiles;
+    const int items = 2 * tiles - split_from;
+    // Expert, first row and channel of item t, its width, and the end of the
+    // expert's rows.  Within an expert groups of raster_gm consecutive M
+    // tiles sweep the N tiles together (M fastest), so that a group's A rows
+    // stay in L2 while B streams past them once.
     struct Place {
-        int e, row, col, row_end;
+        int e, row, col, width, row_end;
     };
     auto locate = [&](int t) {
         Place w;
+        int half = 0;
+        w.width = p.bn;
+        if (t >= split_from) {
+            half = (t - split_from) & 1;
+            t = split_from + ((t - split_from) >> 1);
+            w.width = p.bn / 2;
+        }
         int lo = 0, base = 0, end = p.M;
         if (GROUPED) {
             int hi = p.E;   // list[lo] <= t < list[hi]
@@ -613,7 +632,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int gm = min(tiles_m - m0, p.raster_gm);
         w.e = lo;
         w.row = base + (m0 + in % gm) * 256;
-        w.col = in / gm * BN;
+        w.col = in / gm * p.bn + half * w.width;
         w.row_end = end;
         return w;
     };
@@ -622,27 +641,27 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if (lane == 0) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+            // B rows of a stage: half of the item's columns in each CTA
+            auto load_b = [&](const Place& w, int s, int ks) {
+                if (leader) mbar_arrive_expect_tx(FULL(s), 2u * (uint32_t)I8Pair::stage_bytes(w.width));
+                const int y = w.col + (int)rank * (w.width / 2);
+                tma_load_3d_pair(w.width == p.bn ? &tmB : &tmBh, map_to_rank(FULL(s), 0),
+                                 smem0 + s * stage_bytes + I8_TILE, ks * I8_BK, y, w.e);
+            };
             int stage = 0, pre = 0;
             uint32_t phase = 0;
             bool ok = true;
-            if (!GROUPED && p.b_static && pair < tiles) {
+            if (!GROUPED && p.b_static && pair < items) {
                 // static weights: those of the first stages are requested
                 // before the dependency wait
                 const Place w = locate(pair);
-                for (; pre < STAGES && pre < p.ks_total; ++pre) {
-                    if (leader) mbar_arrive_expect_tx(FULL(pre), 2u * C::STAGE_BYTES);
-                    tma_load_3d_pair(&tmB, map_to_rank(FULL(pre), 0), smem0 + pre * C::STAGE_BYTES + I8_TILE,
-                                     pre * I8_BK, w.col + (int)rank * (BN / 2), w.e);
-                }
+                for (; pre < stages && pre < p.ks_total; ++pre) load_b(w, pre, pre);
             }
             pdl_wait();
-            for (int t = pair; ok && t < tiles; t += npairs) {
+            for (int t = pair; ok && t < items; t += npairs) {
                 const Place w = locate(t);
                 const int ya = w.row + (int)rank * I8_BM;
-                const int yb = w.col + (int)rank * (BN / 2);
                 for (int ks = 0; ks < p.ks_total; ++ks) {
-                    const uint32_t full = map_to_rank(FULL(stage), 0);
-                    const uint32_t st = smem0 + stage * C::STAGE_BYTES;
                     if (pre > 0) {
                         --pre;   // this stage's B tile is on its way
                     } else {
@@ -650,11 +669,10 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             ok = false;
                             break;
                         }
-                        if (leader) mbar_arrive_expect_tx(FULL(stage), 2u * C::STAGE_BYTES);
-                        tma_load_3d_pair(&tmB, full, st + I8_TILE, ks * I8_BK, yb, w.e);
+                        load_b(w, stage, ks);
                     }
-                    tma_load_3d_pair(&tmA, full, st, ks * I8_BK, ya, 0);
-                    if (++stage == STAGES) {
+                    tma_load_3d_pair(&tmA, map_to_rank(FULL(stage), 0), smem0 + stage * stage_bytes, ks * I8_BK, ya, 0);
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -669,21 +687,22 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint64_t adesc0 = desc_sw128(smem0);
             const uint64_t bdesc0 = desc_sw128(smem0 + I8_TILE);
             int stage = 0, buf = 0;
-            for (int t = pair; t < tiles; t += npairs) {
-                const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
+            for (int t = pair; t < items; t += npairs) {
+                const uint32_t acc = tmem_base + (uint32_t)(buf * 256);
+                const uint32_t idesc = idesc_i8(256, t >= split_from ? p.bn / 2 : p.bn);
                 for (int ks = 0; ks < p.ks_total; ++ks) {
                     named_bar_sync(1 + stage, 64);
                     if (lane == 0) {
                         tc_fence_after();
-                        const uint64_t step = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+                        const uint64_t step = (uint64_t)((uint32_t)stage * (stage_bytes >> 4));
 #pragma unroll
                         for (int j = 0; j < I8_BK / I8_MMA_K; ++j)
-                            mma_i8_pair(acc, adesc0 + step + 2 * j, bdesc0 + step + 2 * j, idesc_i8(256, BN),
+                            mma_i8_pair(acc, adesc0 + step + 2 * j, bdesc0 + step + 2 * j, idesc,
                                         (ks > 0 || j > 0) ? 1u : 0u);
                         tc_commit_pair_both(EMPTY(stage));
                     }
                     __syncwarp();
-                    if (++stage == STAGES) stage = 0;
+                    if (++stage == stages) stage = 0;
                 }
                 if (lane == 0) tc_commit_pair_both(ACC_FULL(buf));
                 __syncwarp();
@@ -704,12 +723,12 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int stage = 0, buf = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int t = pair; t < tiles; t += npairs) {
+            for (int t = pair; t < items; t += npairs) {
                 if (ok && !warp_wait(ACC_EMPTY(buf), acc_phase ^ 1u, abort_flag, ERR_ACC_EMPTY)) ok = false;
                 for (int ks = 0; ks < p.ks_total; ++ks) {
                     if (ok && !warp_wait(FULL(stage), phase, abort_flag, ERR_FULL)) ok = false;
                     named_bar_arrive(1 + stage, 64);
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -720,36 +739,31 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp >= 4) {
         const int q = warp & 3;                  // tensor-memory lane quadrant
-        const int half = (warp - 4) >> 2;        // columns [BN/2 half, BN/2 half + BN/2)
-        const int eb = warp - 4;
-        float* sbs = reinterpret_cast<float*>(smem + C::OFF_SCALE) + eb * 256;
+        const int half = (warp - 4) >> 2;        // the warp's 32-column chunks: half, half + 2, ...
+        float* sbs = reinterpret_cast<float*>(smem + I8Pair::OFF_SCALE) + (warp - 4) * 256;
         float* bis = sbs + 128;
         // whole 32-byte sectors where D's rows start on them
         const bool wide = (reinterpret_cast<uintptr_t>(p.D) & 31) == 0 && (p.ldd & 15) == 0;
         pdl_wait();
         uint32_t acc_phase = 0;
         int buf = 0;
-        for (int t = pair; t < tiles; t += npairs) {
+        for (int t = pair; t < items; t += npairs) {
             const Place w = locate(t);
             const int y0 = w.row + (int)rank * I8_BM + q * 32;
-            const int col0 = w.col + half * C::WARP_COLS;
+            const int chunks = (w.width / 32 - half + 1) >> 1;   // 0 to 4
             const float sa = y0 + lane < w.row_end ? __ldcg(p.sa + y0 + lane) : 0.0f;
             const int64_t chan_base = (int64_t)w.e * p.N;
-#pragma unroll
-            for (int i = 0; i < C::WARP_COLS; i += 32) {
-                const int n = col0 + i + lane;
-                sbs[i + lane] = n < p.N ? __ldcg(p.sb + chan_base + n) : 0.0f;
-                bis[i + lane] = n < p.N && p.bias ? __ldcg(p.bias + chan_base + n) : 0.0f;
+            for (int c = 0; c < chunks; ++c) {
+                const int n = w.col + (2 * c + half) * 32 + lane;
+                sbs[c * 32 + lane] = n < p.N ? __ldcg(p.sb + chan_base + n) : 0.0f;
+                bis[c * 32 + lane] = n < p.N && p.bias ? __ldcg(p.bias + chan_base + n) : 0.0f;
             }
             __syncwarp();
             if (!warp_wait(ACC_FULL(buf), acc_phase, abort_flag, ERR_ACC_FULL)) break;
             tc_fence_after();
-            const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + half * C::WARP_COLS);
-            // 32 columns at a time; the next columns' load overlaps this one's arithmetic
-            constexpr int NC = C::WARP_COLS / 32;
-            uint32_t ra[32], rb[32];
+            const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 256 + half * 32);
             auto store = [&](const uint32_t (&r)[32], int c) {
-                const int x0 = col0 + c * 32;
+                const int x0 = w.col + (2 * c + half) * 32;
                 if (y0 >= w.row_end || x0 >= p.N) return;
                 uint32_t packed[16];
 #pragma unroll
@@ -761,7 +775,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     packed[2 * i + 1] = pack16<HALF>(scaled((int)r[4 * i + 2], sa, s4.z, b4.z),
                                                      scaled((int)r[4 * i + 3], sa, s4.w, b4.w));
                 }
-                if (y0 + lane >= w.row_end) return;
+                if (y0 + lane >= w.row_end) return;   // the next expert's row, or none
                 uint16_t* d = p.D + (int64_t)(y0 + lane) * p.ldd + x0;
                 if (x0 + 32 <= p.N && wide) {
                     st_global_v8(d, packed);
@@ -781,27 +795,40 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                 }
             };
-            tmem_ld32(trow, ra);
-            tmem_wait_ld(ra);
-#pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-                tmem_ld32(trow + (c + 1) * 32, rb);
-                store(ra, c);
-                tmem_wait_ld(rb);
-                if (c + 2 < NC) tmem_ld32(trow + (c + 2) * 32, ra);
-                if (c + 2 >= NC) {
-                    // every column is in registers: hand the accumulator back
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader)
-                            mbar_arrive(ACC_EMPTY(buf));
-                        else
-                            mbar_arrive_cluster_relaxed(map_to_rank(ACC_EMPTY(buf), 0));
-                    }
+            // The next chunk's load overlaps this one's arithmetic; once the
+            // last is in registers the accumulator is handed back.
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(ACC_EMPTY(buf));
+                    else
+                        mbar_arrive_cluster_relaxed(map_to_rank(ACC_EMPTY(buf), 0));
                 }
+            };
+            uint32_t ra[32], rb[32];
+            if (chunks > 0) {
+                tmem_ld32(trow, ra);
+                tmem_wait_ld(ra);
+            }
+            if (chunks < 2) release();
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+                if (c >= chunks) break;
+                if (c + 1 < chunks) tmem_ld32(trow + (c + 1) * 64, rb);
+                store(ra, c);
+                __syncwarp();
+                if (c + 1 >= chunks) break;
+                tmem_wait_ld(rb);
+                if (c + 2 < chunks) tmem_ld32(trow + (c + 2) * 64, ra);
+                else release();
                 store(rb, c + 1);
-                if (c + 2 < NC) tmem_wait_ld(ra);
+                __syncwarp();
+                if (c + 2 < chunks) {
+                    tmem_wait_ld(ra);
+                    if (c + 3 >= chunks) release();
+                }
             }
             __syncwarp();   // the scales' memory is written again for the next tile
             buf ^= 1;
@@ -813,8 +840,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     cluster_sync();   // all pair MMAs done, both epilogues finished reading TMEM
     tc_fence_after();
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS)
-                     : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
 }
 
 // ------------------------------------------------------------------------
@@ -894,6 +920,9 @@ I8Params params_of(const Int8GemmArgs& a, int bn)
     p.N = (int32_t)a.N;
     p.ks_total = (int32_t)((a.K + I8_BK - 1) / I8_BK);
     p.tiles_n = (int32_t)((a.N + bn - 1) / bn);
+    p.bn = bn;
+    p.stages = 0;
+    p.halves = 0;
     p.raster_gm = 1;
     p.E = (int32_t)a.E;
     p.offsets = a.offsets;
@@ -924,17 +953,22 @@ cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, cuda
     return e;
 }
 
-template <int BN, bool HALF, bool GROUPED>
-cudaError_t launch_pair(const Int8GemmArgs& a, int64_t tiles, int sm_count, cudaStream_t s)
+template <bool HALF, bool GROUPED>
+cudaError_t launch_pair(const Int8GemmArgs& a, int bn, int64_t tiles, int sm_count, cudaStream_t s)
 {
-    using C = I8PairCfg<BN>;
-    CUtensorMap ta, tb;
+    I8Params p = params_of(a, bn);
+    p.stages = I8Pair::stages(bn);
+    const int64_t pairs = sm_count / 2;
+    const int64_t grid = tiles < pairs ? tiles : pairs;
+    // halves are multiples of 32 columns
+    p.halves = bn % 64 == 0 && (GROUPED || 2 * (tiles % grid) <= grid);
+    CUtensorMap ta, tb, tbh = {};
     if (!make_map_i8(&ta, a.A, 1, a.M, a.K, a.lda, a.lda, I8_BM) ||
-        !make_map_i8(&tb, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, BN / 2)) {
+        !make_map_i8(&tb, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, bn / 2) ||
+        (p.halves && !make_map_i8(&tbh, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, bn / 4))) {
         set_last_error("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
         return cudaErrorInvalidValue;
     }
-    I8Params p = params_of(a, BN);
     // M tiles per group: as many as hold kI8GroupBytes of A, all of them when
     // A fits in half of the L2 cache
     const int64_t tile_bytes = 256 * a.K, tiles_m = (a.M + 255) / 256;
@@ -942,14 +976,13 @@ cudaError_t launch_pair(const Int8GemmArgs& a, int64_t tiles, int sm_count, cuda
     if (tile_bytes * tiles_m > 2 * kI8GroupBytes) rg = (kI8GroupBytes + tile_bytes / 2) / tile_bytes;
     p.raster_gm = (int32_t)(rg < 1 ? 1 : rg > tiles_m ? tiles_m : rg);
     static uint64_t done = 0;
-    auto kern = int8_pair_kernel<BN, HALF, GROUPED>;
-    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), C::SMEM, done);
+    auto kern = int8_pair_kernel<HALF, GROUPED>;
+    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), I8Pair::SMEM, done);
     if (e == cudaSuccess) {
-        const int64_t pairs = sm_count / 2;
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
-        launch_config(cfg, attr, 2u * (unsigned)(tiles < pairs ? tiles : pairs), kI8PairThreads, 2, C::SMEM, s);
-        e = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
+        launch_config(cfg, attr, 2u * (unsigned)grid, kI8PairThreads, 2, I8Pair::SMEM, s);
+        e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tbh, p);
     }
     if (e != cudaSuccess) set_last_error("INT8 GEMM launch (CTA pairs)", e);
     return e;
@@ -961,14 +994,13 @@ cudaError_t launch_swap_t(const Int8GemmArgs& a, int split, int64_t clusters, cu
     return a.half_out ? launch_swap<NT, true>(a, split, clusters, s) : launch_swap<NT, false>(a, split, clusters, s);
 }
 
-template <int BN>
-cudaError_t launch_pair_t(const Int8GemmArgs& a, int64_t tiles, int sm_count, cudaStream_t s)
+cudaError_t launch_pair_t(const Int8GemmArgs& a, int bn, int64_t tiles, int sm_count, cudaStream_t s)
 {
     if (a.offsets)
-        return a.half_out ? launch_pair<BN, true, true>(a, tiles, sm_count, s)
-                          : launch_pair<BN, false, true>(a, tiles, sm_count, s);
-    return a.half_out ? launch_pair<BN, true, false>(a, tiles, sm_count, s)
-                      : launch_pair<BN, false, false>(a, tiles, sm_count, s);
+        return a.half_out ? launch_pair<true, true>(a, bn, tiles, sm_count, s)
+                          : launch_pair<false, true>(a, bn, tiles, sm_count, s);
+    return a.half_out ? launch_pair<true, false>(a, bn, tiles, sm_count, s)
+                      : launch_pair<false, false>(a, bn, tiles, sm_count, s);
 }
 
 // Token tiles of `nt` rows that a launch may need: a grouped one knows only
@@ -999,9 +1031,9 @@ cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo
         return launch_swap_t<128>(a, split, clusters, s);
     }
     const int64_t tm = most_token_tiles(a, 256);
-    const int64_t t256 = tm * ((a.N + 255) / 256), t128 = tm * ((a.N + 127) / 128);
-    if (t256 >= dev.sm_count / 2) return launch_pair_t<256>(a, t256, dev.sm_count, s);
-    return launch_pair_t<128>(a, t128, dev.sm_count, s);
+    int bn = 256;
+    if (tm * ((a.N + 255) / 256) < dev.sm_count / 2) bn = 128;
+    return launch_pair_t(a, bn, tm * ((a.N + bn - 1) / bn), dev.sm_count, s);
 }
 
 cudaError_t read_and_clear_int8_error_word(unsigned int* word)
