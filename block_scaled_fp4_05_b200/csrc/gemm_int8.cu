@@ -26,6 +26,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <mutex>
@@ -197,10 +198,11 @@ __device__ __forceinline__ void expert_bounds(const I8Params& p, int e0, int lan
 //   warp 0     producer: weight and token tiles of each stage by TMA
 //   warp 1     tensor-memory allocation, MMA issue (128 x NT x 32)
 //   warps 2-5  move the accumulator to shared memory as [token][channel]
+//   warps 6-7  only help with the end:
 // then all threads add the S CTAs' sums (integers: any order gives the same
 // result), each CTA for 128 / S channels, scale, and store 8 bytes at a time.
 // ------------------------------------------------------------------------
-constexpr int kSwapThreads = 192;
+constexpr int kSwapThreads = 256;
 
 template <int NT>
 struct SwapCfg {
@@ -219,12 +221,15 @@ struct SwapCfg {
 
 // Adds the S CTAs' sums for this CTA's channels, scales and stores.  A thread
 // has four channels (the same ones for all its tokens) and every
-// (kSwapThreads / pieces)-th token.
+// (kSwapThreads / pieces)-th token, U of them at a time: a read of another
+// CTA's memory takes about a microsecond, so many are kept in flight.
 template <int S, bool HALF>
 __device__ __forceinline__ void swap_finish(const I8Params& p, uint32_t sums, const float* sas, const float* sbs,
                                             int rank, int row0, int ntok, int n0)
 {
     constexpr int PIECES = I8_BM / 4 / S;
+    constexpr int STEP = kSwapThreads / PIECES;
+    constexpr int U = S == 8 ? 1 : S == 4 ? 2 : 4;
     static_assert(kSwapThreads % PIECES == 0, "a thread keeps its channels");
     const int ch = (rank * PIECES + threadIdx.x % PIECES) * 4;   // within the tile
     const int n = n0 + ch;
@@ -234,27 +239,37 @@ __device__ __forceinline__ void swap_finish(const I8Params& p, uint32_t sums, co
     uint32_t from[S];
 #pragma unroll
     for (int r = 0; r < S; ++r) from[r] = map_to_rank(sums + ch * 4u, r);
-    for (int tok = threadIdx.x / PIECES; tok < ntok; tok += kSwapThreads / PIECES) {
-        int4 v[S];
+    for (int tok0 = threadIdx.x / PIECES; tok0 < ntok; tok0 += U * STEP) {
+        int4 v[U][S];
 #pragma unroll
-        for (int r = 0; r < S; ++r) v[r] = ld_cluster_v4(from[r] + (uint32_t)tok * (I8_BM * 4));
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int r = 1; r < S; ++r) {
-            v[0].x += v[r].x;
-            v[0].y += v[r].y;
-            v[0].z += v[r].z;
-            v[0].w += v[r].w;
-        }
-        const float sa = sas[tok];
-        const uint32_t lo = pack16<HALF>(scaled(v[0].x, sa, sb.x, bias.x), scaled(v[0].y, sa, sb.y, bias.y));
-        const uint32_t hi = pack16<HALF>(scaled(v[0].z, sa, sb.z, bias.z), scaled(v[0].w, sa, sb.w, bias.w));
-        uint16_t* d = p.D + (int64_t)(row0 + tok) * p.ldd + n;
-        if (n + 4 <= p.N) {
-            *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
-        } else {
-            d[0] = (uint16_t)lo;
-            if (n + 1 < p.N) d[1] = (uint16_t)(lo >> 16);
-            if (n + 2 < p.N) d[2] = (uint16_t)hi;
+            for (int r = 0; r < S; ++r)
+                if (u == 0 || tok0 + u * STEP < ntok)
+                    v[u][r] = ld_cluster_v4(from[r] + (uint32_t)(tok0 + u * STEP) * (I8_BM * 4));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int tok = tok0 + u * STEP;
+            if (tok >= ntok) break;
+            int4 sum = v[u][0];
+#pragma unroll
+            for (int r = 1; r < S; ++r) {
+                sum.x += v[u][r].x;
+                sum.y += v[u][r].y;
+                sum.z += v[u][r].z;
+                sum.w += v[u][r].w;
+            }
+            const float sa = sas[tok];
+            const uint32_t lo = pack16<HALF>(scaled(sum.x, sa, sb.x, bias.x), scaled(sum.y, sa, sb.y, bias.y));
+            const uint32_t hi = pack16<HALF>(scaled(sum.z, sa, sb.z, bias.z), scaled(sum.w, sa, sb.w, bias.w));
+            uint16_t* d = p.D + (int64_t)(row0 + tok) * p.ldd + n;
+            if (n + 4 <= p.N) {
+                *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+            } else {
+                d[0] = (uint16_t)lo;
+                if (n + 1 < p.N) d[1] = (uint16_t)(lo >> 16);
+                if (n + 2 < p.N) d[2] = (uint16_t)hi;
+            }
         }
     }
 }
@@ -416,7 +431,7 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             tc_commit(acc_full);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 6) {
         pdl_wait();
         const int i = threadIdx.x - 64;
         const int64_t chan = (int64_t)expert * p.N + tn * I8_BM + i;
@@ -446,7 +461,7 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (uint32_t)(c + i) * (I8_BM * 4)), "r"(r[i]) : "memory");
         }
     }
-    if (warp < 2) pdl_wait();   // these warps write D below as well
+    if (warp < 2 || warp >= 6) pdl_wait();   // these warps write D below as well
     tc_fence_before();
     __syncwarp();
     if (split > 1)
@@ -1011,29 +1026,106 @@ int64_t most_token_tiles(const Int8GemmArgs& a, int nt)
     return a.M / nt + (a.E < a.M ? a.E : a.M);
 }
 
+// Estimated microseconds of a product, to choose a kernel and its tile by.
+// Both are bound by what an SM takes in: 107 KB a microsecond at most, less
+// with less of it in flight (a ring of stages turns over in 1.3 us or more).
+// Fitted to times on a B200 over M = 1..8192, N = 320..57344, K = 300..8192,
+// which they meet within about 15 % where HBM does not bind.
+//
+// Few tokens: `tiles` tiles of 128 channels x nt tokens, K split S ways.  The
+// split costs its join, which grows with the tokens.  16x4096x4096: S = 1
+// 12.2, 2 8.6, 4 6.5, 8 6.8 us; 64x4096x4096: 64 tokens S = 1 13.3, 4 8.3,
+// 32 tokens S = 4 7.8 us; 16x28672x8192: S = 1 40.6, 2 45 us.
+constexpr int swap_resident(int nt) { return nt == 16 ? 3 : 2; }   // CTAs an SM
+
+double swap_us(int nt, int split, double tiles, int64_t ks, int sm_count)
+{
+    const double resident = swap_resident(nt);
+    const double ring_kb = nt == 16 ? 72 : nt == 32 ? 100 : 96;
+    const double kb = (double)((ks + split - 1) / split) * (I8_BM + nt) / 8;   // a CTA's operands
+    const double fixed = split == 1   ? 1.7 + 0.010 * nt
+                         : split == 2 ? 2.7 + 0.023 * nt
+                         : split == 4 ? 3.1 + 0.030 * nt
+                                      : 4.1 + 0.044 * nt;
+    const double n = tiles * split / sm_count;   // CTAs an SM
+    if (n <= resident) return fixed + kb / std::fmin(ring_kb / 1.3, 107.0 / std::ceil(n));
+    return 1.15 * n / resident * (fixed + kb / std::fmin(ring_kb / 1.3, 107.0 / resident));
+}
+
+// Many tokens: tiles of 256 tokens x bn channels on the CTA pairs.  A stage
+// takes 0.53 ns x (400 + bn): the tensor pipe's time is proportional to bn,
+// the loads' is not.  301x5003x4099 (2 M tiles): bn = 256 16.5, 160 14.2,
+// 128 (two waves) 20.3 us; 1024x8192x8192: 256 48.9, 224 46.3, 192 63 us.
+double pair_us(int bn, double tiles_m, int64_t N, int64_t ks, int sm_count)
+{
+    const double pairs = sm_count / 2;
+    const double tiles = std::ceil(tiles_m * ((N + bn - 1) / bn));
+    const double full = std::floor(tiles / pairs), rem = tiles - full * pairs;
+    double columns = full * (400 + bn);
+    if (rem > 0) columns += 400 + (full > 0 && bn % 64 == 0 && 2 * rem <= pairs ? bn / 2 : bn);
+    return 3.4 + 0.0085 * bn + 0.00053 * columns * ks;
+}
+
+struct Choice {
+    bool swap;
+    int nt, split, bn;
+};
+
+Choice choose(const Int8GemmArgs& a, int kernel, int sm_count)
+{
+    const int64_t ks = (a.K + I8_BK - 1) / I8_BK, tiles_n = (a.N + I8_BM - 1) / I8_BM;
+    const bool grouped = a.offsets != nullptr;
+    const double mean = grouped ? (double)a.M / a.E : (double)a.M;   // rows an expert
+    const double some = grouped ? (double)(a.E < a.M ? a.E : a.M) : 0;   // experts with rows, at most
+    Choice c = {true, 16, 1, 256};
+    double best_swap = 1e30, best_pair = 1e30;
+    for (int nt = 16; nt <= 128; nt *= 2) {
+        if (nt < 128 && 8 * nt <= mean) continue;
+        // A grouped launch knows only the mean, and experts' shares differ by
+        // several times: an expert of more than nt rows reads its weights
+        // again for each tile, so the tile is wider than the mean.  64 experts
+        // of 2056x2048, 1031 rows unevenly: 16 tokens 46.8, 64 43.1 us; 8 of
+        // 4096x4096, 256 rows: 16 tokens 32.5, 64 25.5 us; but 8 of
+        // 14336x4096, 16 rows: 16 tokens 62, 64 87 us.
+        if (grouped && nt < 64 && nt < 2 * mean && !(nt == 32 && mean <= 20)) continue;
+        if (grouped && nt > 16 && nt > 8 * mean) continue;
+        const double tiles = (grouped ? std::fmax(a.M / nt + 0.5 * some, some) : (double)((a.M + nt - 1) / nt)) * tiles_n;
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (split > ks || tiles * split > swap_resident(nt) * sm_count)) break;
+            const double us = swap_us(nt, split, tiles, ks, sm_count);
+            if (us < best_swap) {
+                best_swap = us;
+                c.nt = nt;
+                c.split = split;
+            }
+        }
+    }
+    // a grouped launch has half an empty tile an expert, on the average
+    const double tiles_m = grouped ? std::ceil(a.M / 256.0 + 0.5 * some) : std::ceil(a.M / 256.0);
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        const double us = pair_us(bn, tiles_m, a.N, ks, sm_count);
+        if (us < best_pair) {
+            best_pair = us;
+            c.bn = bn;
+        }
+    }
+    c.swap = kernel == FP4_GEMM_DECODE || a.K == 0 || (kernel == FP4_GEMM_AUTO && best_swap <= best_pair);
+    return c;
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo& dev, cudaStream_t s)
 {
-    const int64_t per_expert = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
-    bool swap = kernel == FP4_GEMM_DECODE || a.K == 0;
-    if (kernel == FP4_GEMM_AUTO) swap = swap || per_expert <= 128;
-    if (swap) {
-        const int nt = per_expert <= 16 ? 16 : per_expert <= 32 ? 32 : per_expert <= 64 ? 64 : 128;
-        const int64_t tiles_n = (a.N + I8_BM - 1) / I8_BM;
-        const int64_t clusters = most_token_tiles(a, nt) * tiles_n;
-        const int64_t ks = (a.K + I8_BK - 1) / I8_BK;
-        int split = 1;
-        while (split < 8 && clusters * split * 2 <= 2 * dev.sm_count && ks >= 4 * split) split *= 2;
-        if (nt == 16) return launch_swap_t<16>(a, split, clusters, s);
-        if (nt == 32) return launch_swap_t<32>(a, split, clusters, s);
-        if (nt == 64) return launch_swap_t<64>(a, split, clusters, s);
-        return launch_swap_t<128>(a, split, clusters, s);
+    const Choice c = choose(a, kernel, dev.sm_count);
+    if (c.swap) {
+        const int64_t clusters = most_token_tiles(a, c.nt) * ((a.N + I8_BM - 1) / I8_BM);
+        if (c.nt == 16) return launch_swap_t<16>(a, c.split, clusters, s);
+        if (c.nt == 32) return launch_swap_t<32>(a, c.split, clusters, s);
+        if (c.nt == 64) return launch_swap_t<64>(a, c.split, clusters, s);
+        return launch_swap_t<128>(a, c.split, clusters, s);
     }
-    const int64_t tm = most_token_tiles(a, 256);
-    int bn = 256;
-    if (tm * ((a.N + 255) / 256) < dev.sm_count / 2) bn = 128;
-    return launch_pair_t(a, bn, tm * ((a.N + bn - 1) / bn), dev.sm_count, s);
+    return launch_pair_t(a, c.bn, most_token_tiles(a, 256) * ((a.N + c.bn - 1) / c.bn), dev.sm_count, s);
 }
 
 cudaError_t read_and_clear_int8_error_word(unsigned int* word)
