@@ -198,11 +198,13 @@ __device__ __forceinline__ void expert_bounds(const I8Params& p, int e0, int lan
 //   warp 0     producer: weight and token tiles of each stage by TMA
 //   warp 1     tensor-memory allocation, MMA issue (128 x NT x 32)
 //   warps 2-5  move the accumulator to shared memory as [token][channel]
-//   warps 6-7  only help with the end:
+//   warp 7     grouped: finds the next item in the offsets; warps 6 and 7
+//              else only help with the end:
 // then all threads add the S CTAs' sums (integers: any order gives the same
 // result), each CTA for 128 / S channels, scale, and store 8 bytes at a time.
 // ------------------------------------------------------------------------
 constexpr int kSwapThreads = 256;
+constexpr int swap_resident(int nt) { return nt == 16 ? 3 : 2; }   // CTAs an SM holds
 
 template <int NT>
 struct SwapCfg {
@@ -216,7 +218,7 @@ struct SwapCfg {
     static constexpr int SMEM = OFF_SCALE + (NT + 2 * I8_BM) * 4 + 1024;
     static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
     static_assert(NT * I8_BM * 4 <= OFF_BARS, "the sums reuse the stages' memory");
-    static_assert((2 * STAGES + 2) * 8 + 32 <= 256, "barrier area");
+    static_assert((2 * STAGES + 1) * 8 + 40 <= 256, "barrier area");
 };
 
 // Adds the S CTAs' sums for this CTA's channels, scales and stores.  A thread
@@ -287,7 +289,8 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
     // [0,S) full, [S,2S) empty, [2S] accumulator full
     int* shared_word = reinterpret_cast<int*>(bars + 2 * STAGES + 1);
-    // [0] tensor-memory base, [1] abort, [2..5] expert, first row, rows, tile within the expert
+    // [0] tensor-memory base, [1] abort; [2..5] and [6..9] the item (grouped,
+    // even and odd ones): expert (-1: none), first row, rows, tile within the expert
     volatile int* abort_flag = shared_word + 1;
     float* sas = reinterpret_cast<float*>(smem + C::OFF_SCALE);   // [NT]
     float* sbs = sas + NT;                                        // [128], then the bias [128]
@@ -304,9 +307,14 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     auto FULL = [&](int s) { return bar0 + 8u * s; };
     auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
     const uint32_t acc_full = bar0 + 8u * (2 * STAGES);
+    // Items: the tiles (expert, channel tile, token tile), token tiles
+    // fastest so that clusters that share weights run next to each other,
+    // dealt round-robin to the clusters.
+    const int cluster = (int)(blockIdx.x / split), clusters = (int)(gridDim.x / split);
+    const int dense_mt = (p.M + NT - 1) / NT;
     // Weight tiles requested before the dependency wait (static weights of a
     // dense product): those of the first stages, their token tiles follow.
-    const int pre = !p.offsets && p.b_static ? min(STAGES, ke - kb) : 0;
+    int pre = !p.offsets && p.b_static ? min(STAGES, ke - kb) : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -317,45 +325,10 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (pre > 0) {
-            const int mt = (p.M + NT - 1) / NT;
-            const int tn = (int)(blockIdx.x / split) / mt;
-            for (int i = 0; i < pre; ++i) {
-                mbar_arrive_expect_tx(FULL(i), C::STAGE_BYTES);
-                tma_load_3d(&tmW, FULL(i), smem0 + i * C::STAGE_BYTES, (kb + i) * I8_BK, tn * I8_BM, 0);
-            }
+        for (int i = 0; i < pre; ++i) {
+            mbar_arrive_expect_tx(FULL(i), C::STAGE_BYTES);
+            tma_load_3d(&tmW, FULL(i), smem0 + i * C::STAGE_BYTES, (kb + i) * I8_BK, cluster / dense_mt * I8_BM, 0);
         }
-    }
-    // The tile: cluster c takes the c-th of the list (expert, channel tile,
-    // token tile), token tiles fastest, so that the CTAs that share weights
-    // run next to each other.
-    if (p.offsets) {
-        if (warp == 0) {
-            __syncwarp();
-            pdl_wait();
-            const int64_t c = blockIdx.x / split;
-            int64_t seen = 0;   // tiles of the experts before e0
-            int reached = 0, found = 0;
-            for (int e0 = 0; e0 < p.E && !found; e0 += 32) {
-                int first, end;
-                expert_bounds(p, e0, lane, reached, first, end);
-                const int mt = (end - first + NT - 1) / NT;
-                const int upto = warp_scan_add(mt, lane);   // token tiles up to this expert
-                const bool mine = c < seen + (int64_t)upto * p.tiles_n &&
-                                  c >= seen + (int64_t)(upto - mt) * p.tiles_n;
-                if (mine) {
-                    shared_word[2] = e0 + lane;
-                    shared_word[3] = first;
-                    shared_word[4] = end - first;
-                    shared_word[5] = (int)(c - seen - (int64_t)(upto - mt) * p.tiles_n);
-                }
-                found = __any_sync(0xFFFFFFFFu, mine);
-                seen += (int64_t)__shfl_sync(0xFFFFFFFFu, upto, 31) * p.tiles_n;
-            }
-            if (!found && lane == 0) shared_word[2] = -1;
-        }
-        __syncthreads();
-        if (shared_word[2] < 0) return;   // no such tile: the whole cluster leaves
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -364,126 +337,166 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    // Item c of a grouped launch, found by one warp (into the words of its parity).
+    auto find_item = [&](int64_t c, int odd) {
+        int* word = shared_word + 2 + 4 * odd;
+        int64_t seen = 0;   // tiles of the experts before e0
+        int reached = 0, found = 0;
+        for (int e0 = 0; e0 < p.E && !found; e0 += 32) {
+            int first, end;
+            expert_bounds(p, e0, lane, reached, first, end);
+            const int mt = (end - first + NT - 1) / NT;
+            const int upto = warp_scan_add(mt, lane);   // token tiles up to this expert
+            const int64_t from = seen + (int64_t)(upto - mt) * p.tiles_n;
+            const bool mine = c >= from && c < from + (int64_t)mt * p.tiles_n;
+            if (mine) {
+                word[0] = e0 + lane;
+                word[1] = first;
+                word[2] = end - first;
+                word[3] = (int)(c - from);
+            }
+            found = __any_sync(0xFFFFFFFFu, mine);
+            seen += (int64_t)__shfl_sync(0xFFFFFFFFu, upto, 31) * p.tiles_n;
+        }
+        if (!found && lane == 0) word[0] = -1;
+    };
+    __syncwarp();
+    if (p.offsets && warp == 7) {
+        pdl_wait();
+        find_item(cluster, 0);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = (uint32_t)shared_word[0];
-    int expert = 0, first = 0, rows = p.M, tile = (int)(blockIdx.x / split);
-    if (p.offsets) {
-        expert = shared_word[2];
-        first = shared_word[3];
-        rows = shared_word[4];
-        tile = shared_word[5];
-    }
-    const int mt = (rows + NT - 1) / NT;
-    const int tm = tile % mt, tn = tile / mt;
-    const int row0 = first + tm * NT;        // first token
-    const int ntok = min(NT, rows - tm * NT);
+    pdl_trigger();
+    pdl_wait();
 
-    if (warp == 0) {
-        if (lane == 0 && kb < ke) {
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmX)) : "memory");
-            pdl_trigger();
-            pdl_wait();
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int ks = kb; ks < ke; ++ks) {
-                const uint32_t st = smem0 + stage * C::STAGE_BYTES;
-                if (ks - kb >= pre) {
-                    if (!wait_fast(EMPTY(stage), phase ^ 1u, abort_flag, ERR_EMPTY)) {
-                        ok = false;
-                        break;
+    int stage = 0, odd = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    for (int64_t c = cluster;; c += clusters, odd ^= 1) {
+        int expert = 0, first = 0, rows = p.M, tile = (int)c;
+        if (p.offsets) {
+            const int* word = shared_word + 2 + 4 * odd;
+            expert = word[0];
+            first = word[1];
+            rows = word[2];
+            tile = word[3];
+            if (expert < 0) break;   // no rows at all (the same in every CTA of the cluster)
+        }
+        const int mt = (rows + NT - 1) / NT;
+        const int tm = tile % mt, tn = tile / mt;
+        const int row0 = first + tm * NT;        // first token
+        const int ntok = min(NT, rows - tm * NT);
+
+        if (warp == 0) {
+            if (lane == 0) {
+                bool ok = true;
+                for (int ks = kb; ks < ke; ++ks) {
+                    const uint32_t st = smem0 + stage * C::STAGE_BYTES;
+                    if (pre > 0) {
+                        --pre;   // this stage's weight tile is on its way
+                    } else {
+                        if (!wait_fast(EMPTY(stage), phase ^ 1u, abort_flag, ERR_EMPTY)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(FULL(stage), C::STAGE_BYTES);
+                        tma_load_3d(&tmW, FULL(stage), st, ks * I8_BK, tn * I8_BM, expert);
                     }
-                    mbar_arrive_expect_tx(FULL(stage), C::STAGE_BYTES);
-                    tma_load_3d(&tmW, FULL(stage), st, ks * I8_BK, tn * I8_BM, expert);
+                    tma_load_2d(&tmX, FULL(stage), st + C::OFF_T, ks * I8_BK, row0);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                tma_load_2d(&tmX, FULL(stage), st + C::OFF_T, ks * I8_BK, row0);
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                if (!ok || *abort_flag) spin_ns(200000);   // loads in flight land before the memory is used again
             }
-            if (!ok || *abort_flag) spin_ns(200000);   // loads in flight land before the memory is used again
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0 && kb < ke) {
-            const uint64_t adesc0 = desc_sw128(smem0);
-            const uint64_t bdesc0 = desc_sw128(smem0 + C::OFF_T);
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int ks = kb; ks < ke; ++ks) {
-                if (!wait_fast(FULL(stage), phase, abort_flag, ERR_FULL)) break;
-                tc_fence_after();
-                const uint64_t step = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+            __syncwarp();
+        } else if (warp == 1) {
+            if (lane == 0 && kb < ke) {
+                const uint64_t adesc0 = desc_sw128(smem0);
+                const uint64_t bdesc0 = desc_sw128(smem0 + C::OFF_T);
+                for (int ks = kb; ks < ke; ++ks) {
+                    if (!wait_fast(FULL(stage), phase, abort_flag, ERR_FULL)) break;
+                    tc_fence_after();
+                    const uint64_t step = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
 #pragma unroll
-                for (int j = 0; j < I8_BK / I8_MMA_K; ++j)
-                    mma_i8(tmem_base, adesc0 + step + 2 * j, bdesc0 + step + 2 * j, idesc_i8(I8_BM, NT),
-                           (ks > kb || j > 0) ? 1u : 0u);
-                tc_commit(EMPTY(stage));
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
+                    for (int j = 0; j < I8_BK / I8_MMA_K; ++j)
+                        mma_i8(tmem_base, adesc0 + step + 2 * j, bdesc0 + step + 2 * j, idesc_i8(I8_BM, NT),
+                               (ks > kb || j > 0) ? 1u : 0u);
+                    tc_commit(EMPTY(stage));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
+                // completes when every MMA issued here has
+                tc_commit(acc_full);
             }
-            // completes when every MMA issued here has
-            tc_commit(acc_full);
+            __syncwarp();
+        } else if (warp < 6) {
+            const int i = threadIdx.x - 64;
+            const int64_t chan = (int64_t)expert * p.N + tn * I8_BM + i;
+            const bool in = tn * I8_BM + i < p.N;
+            if (i < ntok) sas[i] = __ldcg(p.sa + row0 + i);
+            sbs[i] = in ? __ldcg(p.sb + chan) : 0.0f;
+            sbs[I8_BM + i] = in && p.bias ? __ldcg(p.bias + chan) : 0.0f;
+            const int q = warp & 3;   // tensor-memory lane quadrant: channels [32 q, 32 q + 32)
+            const uint32_t dst = smem0 + (uint32_t)(q * 32 + lane) * 4u;
+            const bool have = kb < ke && warp_wait(acc_full, acc_phase, abort_flag, ERR_ACC_FULL);
+            acc_phase ^= 1u;
+            tc_fence_after();
+            // Every stage has been read by then (the MMAs are complete) and
+            // none is being filled, so the sums take their place.
+#pragma unroll
+            for (int col = 0; col < NT; col += 16) {
+                if (col >= ntok) break;
+                uint32_t r[16];
+                if (have) {
+                    tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + col, r);
+                    tmem_wait_ld(r);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) r[k] = 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (uint32_t)(col + k) * (I8_BM * 4)), "r"(r[k])
+                                 : "memory");
+            }
+        } else if (warp == 7 && p.offsets) {
+            find_item(c + clusters, odd ^ 1);
         }
+        tc_fence_before();
         __syncwarp();
-    } else if (warp < 6) {
-        pdl_wait();
-        const int i = threadIdx.x - 64;
-        const int64_t chan = (int64_t)expert * p.N + tn * I8_BM + i;
-        const bool in = tn * I8_BM + i < p.N;
-        if (i < ntok) sas[i] = __ldcg(p.sa + row0 + i);
-        sbs[i] = in ? __ldcg(p.sb + chan) : 0.0f;
-        sbs[I8_BM + i] = in && p.bias ? __ldcg(p.bias + chan) : 0.0f;
-        const int q = warp & 3;   // tensor-memory lane quadrant: channels [32 q, 32 q + 32)
-        const uint32_t dst = smem0 + (uint32_t)(q * 32 + lane) * 4u;
-        const bool have = kb < ke && warp_wait(acc_full, 0, abort_flag, ERR_ACC_FULL);
+        if (split > 1)
+            cluster_sync();
+        else
+            __syncthreads();
         tc_fence_after();
-        // Every stage has been read by then (the MMAs are complete), so the
-        // sums take their place.
-#pragma unroll
-        for (int c = 0; c < NT; c += 16) {
-            if (c >= ntok) break;
-            uint32_t r[16];
-            if (have) {
-                tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
-                tmem_wait_ld(r);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (uint32_t)(c + i) * (I8_BM * 4)), "r"(r[i]) : "memory");
-        }
+        if (split == 1)
+            swap_finish<1, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+        else if (split == 2)
+            swap_finish<2, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+        else if (split == 4)
+            swap_finish<4, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+        else
+            swap_finish<8, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
+        const bool more = p.offsets ? shared_word[2 + 4 * (odd ^ 1)] >= 0 : c + clusters < (int64_t)dense_mt * p.tiles_n;
+        // The sums have been read, by the other CTAs too, before the next
+        // item's loads (or this CTA's end) touch their memory.
+        if (more) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (split > 1)
+            cluster_sync();
+        else if (more)
+            __syncthreads();
+        if (!more) break;
     }
-    if (warp < 2 || warp >= 6) pdl_wait();   // these warps write D below as well
-    tc_fence_before();
-    __syncwarp();
-    if (split > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    tc_fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS)
                      : "memory");
-    if (split == 1)
-        swap_finish<1, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
-    else if (split == 2)
-        swap_finish<2, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
-    else if (split == 4)
-        swap_finish<4, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
-    else
-        swap_finish<8, HALF>(p, smem0, sas, sbs, rank, row0, ntok, tn * I8_BM);
-    if (split > 1) {
-        __syncwarp();
-        cluster_sync();   // no CTA leaves while another reads its sums
-    }
 }
 
 // ------------------------------------------------------------------------
@@ -946,7 +959,7 @@ I8Params params_of(const Int8GemmArgs& a, int bn)
 }
 
 template <int NT, bool HALF>
-cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, cudaStream_t s)
+cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, int sm_count, cudaStream_t s)
 {
     using C = SwapCfg<NT>;
     CUtensorMap tw = {}, tx = {};
@@ -961,7 +974,9 @@ cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, cuda
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
-        launch_config(cfg, attr, (unsigned)(clusters * split), kSwapThreads, (unsigned)split, C::SMEM, s);
+        // as many clusters as the SMs hold take all tiles in turn
+        const int64_t hold = (int64_t)swap_resident(NT) * sm_count / split;
+        launch_config(cfg, attr, (unsigned)((clusters < hold ? clusters : hold) * split), kSwapThreads, (unsigned)split, C::SMEM, s);
         e = cudaLaunchKernelEx(&cfg, kern, tw, tx, params_of(a, I8_BM));
     }
     if (e != cudaSuccess) set_last_error("INT8 GEMM launch (few tokens)", e);
@@ -1004,9 +1019,10 @@ cudaError_t launch_pair(const Int8GemmArgs& a, int bn, int64_t tiles, int sm_cou
 }
 
 template <int NT>
-cudaError_t launch_swap_t(const Int8GemmArgs& a, int split, int64_t clusters, cudaStream_t s)
+cudaError_t launch_swap_t(const Int8GemmArgs& a, int split, int64_t clusters, int sm_count, cudaStream_t s)
 {
-    return a.half_out ? launch_swap<NT, true>(a, split, clusters, s) : launch_swap<NT, false>(a, split, clusters, s);
+    return a.half_out ? launch_swap<NT, true>(a, split, clusters, sm_count, s)
+                      : launch_swap<NT, false>(a, split, clusters, sm_count, s);
 }
 
 cudaError_t launch_pair_t(const Int8GemmArgs& a, int bn, int64_t tiles, int sm_count, cudaStream_t s)
@@ -1036,8 +1052,6 @@ int64_t most_token_tiles(const Int8GemmArgs& a, int nt)
 // split costs its join, which grows with the tokens.  16x4096x4096: S = 1
 // 12.2, 2 8.6, 4 6.5, 8 6.8 us; 64x4096x4096: 64 tokens S = 1 13.3, 4 8.3,
 // 32 tokens S = 4 7.8 us; 16x28672x8192: S = 1 40.6, 2 45 us.
-constexpr int swap_resident(int nt) { return nt == 16 ? 3 : 2; }   // CTAs an SM
-
 double swap_us(int nt, int split, double tiles, int64_t ks, int sm_count)
 {
     const double resident = swap_resident(nt);
@@ -1109,6 +1123,12 @@ Choice choose(const Int8GemmArgs& a, int kernel, int sm_count)
             c.bn = bn;
         }
     }
+    // Where the weights' bytes bind, the few-token kernel reads them at 5.8
+    // TB/s or more and the pair kernel, whose tiles are partly empty then, at
+    // 5.0 (64 experts of 2056x2048, 1031 rows: 48 against 56 us).
+    const double weight_mb = 1e-6 * (grouped ? some : 1) * (double)a.N * (double)a.K;
+    best_swap = std::fmax(best_swap, weight_mb / 5.8 + 2);
+    best_pair = std::fmax(best_pair, weight_mb / 5.0 + 4);
     c.swap = kernel == FP4_GEMM_DECODE || a.K == 0 || (kernel == FP4_GEMM_AUTO && best_swap <= best_pair);
     return c;
 }
@@ -1120,10 +1140,10 @@ cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo
     const Choice c = choose(a, kernel, dev.sm_count);
     if (c.swap) {
         const int64_t clusters = most_token_tiles(a, c.nt) * ((a.N + I8_BM - 1) / I8_BM);
-        if (c.nt == 16) return launch_swap_t<16>(a, c.split, clusters, s);
-        if (c.nt == 32) return launch_swap_t<32>(a, c.split, clusters, s);
-        if (c.nt == 64) return launch_swap_t<64>(a, c.split, clusters, s);
-        return launch_swap_t<128>(a, c.split, clusters, s);
+        if (c.nt == 16) return launch_swap_t<16>(a, c.split, clusters, dev.sm_count, s);
+        if (c.nt == 32) return launch_swap_t<32>(a, c.split, clusters, dev.sm_count, s);
+        if (c.nt == 64) return launch_swap_t<64>(a, c.split, clusters, dev.sm_count, s);
+        return launch_swap_t<128>(a, c.split, clusters, dev.sm_count, s);
     }
     return launch_pair_t(a, c.bn, most_token_tiles(a, 256) * ((a.N + c.bn - 1) / c.bn), dev.sm_count, s);
 }
