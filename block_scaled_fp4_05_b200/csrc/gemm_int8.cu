@@ -125,12 +125,23 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr)
     return v;
 }
 
-// 32 bytes, 32-byte aligned.
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v)
+// One step of a 4 x 4 transposition of 16-byte pieces (v[4 j .. 4 j + 3] is
+// piece j) among the lanes of a quad: pieces and lanes whose numbers differ in
+// bit `bit` (1 or 2) change places.
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[16], int lane, int bit)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+    const bool upper = lane & bit;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j & bit) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t &lo = v[4 * j + i], &hi = v[4 * (j | bit) + i];
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? lo : hi, bit);
+            if (upper) lo = got;
+            else hi = got;
+        }
+    }
 }
 
 template <bool HALF>
@@ -514,17 +525,20 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 //               for each stage, then opens the stage's named barrier
 //   warp 3      grouped: the tile list from the offsets
 //   warps 4-11  epilogue: two warps a tensor-memory lane quadrant, 32 columns
-//               in turn; scales, bias, 16 bits, and from the registers to D
-//               in whole 32-byte sectors, a lane a row
+//               in turn; scales, bias, 16 bits, and from the registers to D,
+//               four lanes a row (sixteen warps were 10 % faster where the
+//               sums are short, K = 128 to 512, and 0.5 us slower a launch)
 // Every wait is bounded; a CTA that gives up records it in the error word.
 // ------------------------------------------------------------------------
-constexpr int kI8PairThreads = 384;
 constexpr int kI8EpiWarps = 8;
+constexpr int kI8Parts = kI8EpiWarps / 4;        // epilogue warps a tensor-memory lane quadrant
+constexpr int kI8Chunks = 256 / 32 / kI8Parts;   // 32-column chunks of each
+constexpr int kI8PairThreads = 128 + 32 * kI8EpiWarps;
 constexpr int kI8PairMaxStages = 12;
 
 struct I8Pair {
     static constexpr int OFF_SCALE = 0;                                            // sB and bias of a warp's columns
-    static constexpr int OFF_LIST = OFF_SCALE + kI8EpiWarps * 2 * 128 * 4;         // experts' first tiles and bounds
+    static constexpr int OFF_LIST = OFF_SCALE + 4 * 2 * 256 * 4;          // experts' first tiles and bounds
     static constexpr int OFF_BARS = OFF_LIST + 2 * (kMaxExperts + 2) * 4;
     static constexpr int NBARS = 2 * kI8PairMaxStages + 5;
     static constexpr int FIXED = (OFF_BARS + 256 + 1023) / 1024 * 1024;            // what lies before the stages
@@ -767,98 +781,98 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp >= 4) {
         const int q = warp & 3;                  // tensor-memory lane quadrant
-        const int half = (warp - 4) >> 2;        // the warp's 32-column chunks: half, half + 2, ...
-        float* sbs = reinterpret_cast<float*>(smem + I8Pair::OFF_SCALE) + (warp - 4) * 256;
-        float* bis = sbs + 128;
-        // whole 32-byte sectors where D's rows start on them
-        const bool wide = (reinterpret_cast<uintptr_t>(p.D) & 31) == 0 && (p.ldd & 15) == 0;
+        const int part = (warp - 4) >> 2;        // the warp's 32-column chunks: part, part + kI8Parts, ...
+        float* sbs = reinterpret_cast<float*>(smem + I8Pair::OFF_SCALE) + (warp - 4) * (2 * 32 * kI8Chunks);
+        float* bis = sbs + 32 * kI8Chunks;
         pdl_wait();
+        // The scales of an item (this lane's row, a column of each chunk) are
+        // read while the item before it is worked on.
+        Place next = {};
+        float sa_next = 0.0f, sb_next[kI8Chunks] = {}, bias_next[kI8Chunks] = {};
+        auto fetch = [&](int t) {
+            if (t >= items) return;
+            next = locate(t);
+            const int y = next.row + (int)rank * I8_BM + q * 32 + lane;
+            if (y < next.row_end) sa_next = __ldcg(p.sa + y);
+            const int64_t chan_base = (int64_t)next.e * p.N;
+#pragma unroll
+            for (int c = 0; c < kI8Chunks; ++c) {
+                const int n = next.col + (part + kI8Parts * c) * 32 + lane;
+                const bool in = (part + kI8Parts * c) * 32 < next.width && n < p.N;
+                sb_next[c] = in ? __ldcg(p.sb + chan_base + n) : 0.0f;
+                bias_next[c] = in && p.bias ? __ldcg(p.bias + chan_base + n) : 0.0f;
+            }
+        };
+        fetch(pair);
         uint32_t acc_phase = 0;
         int buf = 0;
         for (int t = pair; t < items; t += npairs) {
-            const Place w = locate(t);
-            const int y0 = w.row + (int)rank * I8_BM + q * 32;
-            const int chunks = (w.width / 32 - half + 1) >> 1;   // 0 to 4
-            const float sa = y0 + lane < w.row_end ? __ldcg(p.sa + y0 + lane) : 0.0f;
-            const int64_t chan_base = (int64_t)w.e * p.N;
-            for (int c = 0; c < chunks; ++c) {
-                const int n = w.col + (2 * c + half) * 32 + lane;
-                sbs[c * 32 + lane] = n < p.N ? __ldcg(p.sb + chan_base + n) : 0.0f;
-                bis[c * 32 + lane] = n < p.N && p.bias ? __ldcg(p.bias + chan_base + n) : 0.0f;
+            const Place w = next;
+            const float sa = sa_next;
+#pragma unroll
+            for (int c = 0; c < kI8Chunks; ++c) {
+                sbs[c * 32 + lane] = sb_next[c];
+                bis[c * 32 + lane] = bias_next[c];
             }
             __syncwarp();
+            fetch(t + npairs);
+            const int y0 = w.row + (int)rank * I8_BM + q * 32;
+            const int chunks = (w.width / 32 - part + kI8Parts - 1) / kI8Parts;   // 0 to kI8Chunks
             if (!warp_wait(ACC_FULL(buf), acc_phase, abort_flag, ERR_ACC_FULL)) break;
             tc_fence_after();
-            const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 256 + half * 32);
-            auto store = [&](const uint32_t (&r)[32], int c) {
-                const int x0 = w.col + (2 * c + half) * 32;
-                if (y0 >= w.row_end || x0 >= p.N) return;
-                uint32_t packed[16];
+            const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 256 + part * 32);
+            uint32_t r2[2][32];
+            if (chunks > 0) tmem_ld32(trow, r2[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 s4 = *reinterpret_cast<const float4*>(sbs + c * 32 + 4 * i);
-                    const float4 b4 = *reinterpret_cast<const float4*>(bis + c * 32 + 4 * i);
-                    packed[2 * i] = pack16<HALF>(scaled((int)r[4 * i], sa, s4.x, b4.x),
-                                                 scaled((int)r[4 * i + 1], sa, s4.y, b4.y));
-                    packed[2 * i + 1] = pack16<HALF>(scaled((int)r[4 * i + 2], sa, s4.z, b4.z),
-                                                     scaled((int)r[4 * i + 3], sa, s4.w, b4.w));
-                }
-                if (y0 + lane >= w.row_end) return;   // the next expert's row, or none
-                uint16_t* d = p.D + (int64_t)(y0 + lane) * p.ldd + x0;
-                if (x0 + 32 <= p.N && wide) {
-                    st_global_v8(d, packed);
-                    st_global_v8(d + 16, packed + 8);
-                    return;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (x0 + 8 * j + 8 <= p.N) {
-                        *reinterpret_cast<uint4*>(d + 8 * j) = make_uint4(packed[4 * j], packed[4 * j + 1],
-                                                                          packed[4 * j + 2], packed[4 * j + 3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (x0 + 8 * j + i < p.N)
-                                d[8 * j + i] = (uint16_t)(packed[4 * j + (i >> 1)] >> (16 * (i & 1)));
+            for (int c = 0; c < kI8Chunks; ++c) {
+                uint32_t (&r)[32] = r2[c & 1];
+                if (c < chunks) tmem_wait_ld(r);
+                if (c + 1 < chunks) {   // the next chunk's load overlaps this one's arithmetic
+                    tmem_ld32(trow + (uint32_t)((c + 1) * kI8Parts * 32), r2[(c + 1) & 1]);
+                } else if (c == max(chunks - 1, 0)) {
+                    // every column is in registers: hand the accumulator back
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader)
+                            mbar_arrive(ACC_EMPTY(buf));
+                        else
+                            mbar_arrive_cluster_relaxed(map_to_rank(ACC_EMPTY(buf), 0));
                     }
                 }
-            };
-            // The next chunk's load overlaps this one's arithmetic; once the
-            // last is in registers the accumulator is handed back.
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader)
-                        mbar_arrive(ACC_EMPTY(buf));
-                    else
-                        mbar_arrive_cluster_relaxed(map_to_rank(ACC_EMPTY(buf), 0));
-                }
-            };
-            uint32_t ra[32], rb[32];
-            if (chunks > 0) {
-                tmem_ld32(trow, ra);
-                tmem_wait_ld(ra);
-            }
-            if (chunks < 2) release();
+                const int x0 = w.col + (part + kI8Parts * c) * 32;
+                if (c < chunks && y0 < w.row_end && x0 < p.N) {
+                    uint32_t v[16];
 #pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-                if (c >= chunks) break;
-                if (c + 1 < chunks) tmem_ld32(trow + (c + 1) * 64, rb);
-                store(ra, c);
-                __syncwarp();
-                if (c + 1 >= chunks) break;
-                tmem_wait_ld(rb);
-                if (c + 2 < chunks) tmem_ld32(trow + (c + 2) * 64, ra);
-                else release();
-                store(rb, c + 1);
-                __syncwarp();
-                if (c + 2 < chunks) {
-                    tmem_wait_ld(ra);
-                    if (c + 3 >= chunks) release();
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 s4 = *reinterpret_cast<const float4*>(sbs + c * 32 + 4 * i);
+                        const float4 b4 = *reinterpret_cast<const float4*>(bis + c * 32 + 4 * i);
+                        v[2 * i] = pack16<HALF>(scaled((int)r[4 * i], sa, s4.x, b4.x),
+                                                scaled((int)r[4 * i + 1], sa, s4.y, b4.y));
+                        v[2 * i + 1] = pack16<HALF>(scaled((int)r[4 * i + 2], sa, s4.z, b4.z),
+                                                    scaled((int)r[4 * i + 3], sa, s4.w, b4.w));
+                    }
+                    // Four lanes exchange their rows' 16-byte pieces, so that
+                    // lane i has piece i of all four rows and they store 64
+                    // bytes of one row at a time.
+                    quad_transpose(v, lane, 1);
+                    quad_transpose(v, lane, 2);
+                    const int x = x0 + 8 * (lane & 3);
+                    uint16_t* d = p.D + (int64_t)(y0 + (lane & 28)) * p.ldd + x;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k, d += p.ldd) {
+                        if (y0 + (lane & 28) + k >= w.row_end) break;   // the next expert's row, or none
+                        if (x + 8 <= p.N) {
+                            *reinterpret_cast<uint4*>(d) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (x + i < p.N) d[i] = (uint16_t)(v[4 * k + (i >> 1)] >> (16 * (i & 1)));
+                        }
+                    }
                 }
+                __syncwarp();   // (after the last chunk: the scales' memory is written again)
             }
-            __syncwarp();   // the scales' memory is written again for the next tile
             buf ^= 1;
             if (buf == 0) acc_phase ^= 1u;
         }
