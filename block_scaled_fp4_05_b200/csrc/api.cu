@@ -99,6 +99,7 @@ constexpr int64_t kMaxRowTiles = (int64_t)1 << 28;
 constexpr int64_t kInt8MaxK = 131071;
 constexpr int64_t kMaxInt8Tiles = (int64_t)1 << 26;   // of 256 x 128; D has terabytes there
 constexpr int64_t kMaxMapStride = (int64_t)1 << 40;
+constexpr int64_t kMaxInt8Cols = (int64_t)1 << 30;   // the quantizer indexes a row in 32 bits
 
 }  // namespace
 
@@ -577,7 +578,7 @@ fp4_status fp4_quantize_int8(const void* in, fp4_dtype in_dtype, int64_t rows_in
     if (!row_index && rows != rows_in) return FP4_ERR_INVALID_ARG;
     if (rows == 0) return FP4_OK;
     if (!scales_out || (cols > 0 && (!codes_out || (rows_in > 0 && !in)))) return FP4_ERR_INVALID_ARG;
-    if (rows >= kMaxRows || rows_in >= kMaxRows || cols >= kMaxRows) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (rows >= kMaxRows || rows_in >= kMaxRows || cols > kMaxInt8Cols) return FP4_ERR_UNSUPPORTED_SHAPE;
     if (ld % 8 != 0 || ld_codes % 16 != 0 || !aligned16(in) || !aligned16(codes_out) || !aligned4(scales_out) ||
         !aligned4(row_index))
         return FP4_ERR_MISALIGNED;

@@ -9,10 +9,11 @@
 // between two integers or at least 2^-19 (relative) away from it; an FP32
 // quotient within an ulp rounds to the same integer unless it is a tie, and a
 // tie has to come out exact.  With the row scaled by a power of two (exact,
-// so that neither 127 x nor 1 / amax leaves the FP32 range) and r = RN(1/amax):
+// so that neither 127 x nor 1 / amax leaves the FP32 range) and r the
+// approximate reciprocal of amax (within 2^-22 of it):
 //   t = RN(a r), a = 127 x;  e = a - t amax (exact as an FMA: it cancels to a
 //   few bits);  q = RN(t + e r)
-// t + e r differs from the quotient by less than 2^-44 of it, so a quotient
+// t + e r differs from the quotient by less than 2^-42 of it, so a quotient
 // that FP32 holds (every tie does) comes out exactly.  Adding 1.5 * 2^23 rounds
 // q to an integer, halves to even, and leaves its two's complement in the low
 // byte.  Two elements go through these steps in one instruction each.
@@ -21,7 +22,11 @@
 // registers of its threads between the maximum and the codes, so it is read
 // once; rows above 32768 elements are read twice (the second time mostly from
 // L2).  Short-lived blocks, one row each (a warp a row up to 2048 elements),
-// keep more loads in flight than a resident ring would.
+// keep more loads in flight than blocks that load a row ahead while they work
+// on one (8194 rows of 4096: 18.9, two rows a block 19.5, eight 21.7 us).
+// Measured on a B200, of 6559 GB/s: 8192x8192 31.1 us (99 %), 8194x4096 16.3
+// us (94 %); 8194 rows gathered from 4097 of 4096 17.2 us, where instructions
+// bind (about ten an element, 70 % of the issue slots).
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -38,8 +43,7 @@ namespace {
 struct RowScale {
     float c;      // 127 * 2^p
     float m;      // amax * 2^p
-    float r;      // RN(1 / m)
-    float scale;  // what the codes are to be multiplied by
+    float r;      // about 1 / m
 };
 
 template <bool HALF>
@@ -48,36 +52,30 @@ __device__ __forceinline__ float widen(uint32_t bits16)
     return HALF ? __half2float(__ushort_as_half((unsigned short)bits16)) : __uint_as_float(bits16 << 16);
 }
 
-// amax_bits: the largest magnitude of the row as its 16-bit pattern.
+// amax_bits: the largest magnitude of the row as its 16-bit pattern, finite.
 template <bool HALF>
 __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits)
 {
     RowScale s;
-    const uint32_t inf = HALF ? 0x7C00u : 0x7F80u;
-    if (amax_bits == 0u) {
-        s.c = 0.0f;
-        s.m = 1.0f;
-        s.r = 1.0f;
-        s.scale = 1.0f;
-        return s;
-    }
-    if (amax_bits >= inf) {   // the products of the row come out NaN
-        s.c = 0.0f;
-        s.m = 1.0f;
-        s.r = 1.0f;
-        s.scale = __uint_as_float(0x7FC00000u);
-        return s;
-    }
     const float amax = widen<HALF>(amax_bits);
     // 2^p brings a normal maximum into [4, 8); p is capped at 120, so that
     // 127 * 2^p is finite (subnormal BF16 maxima then end below 4)
     const int eb = (int)(__float_as_uint(amax) >> 23);
     const float p = __uint_as_float((uint32_t)min(256 - eb, 247) << 23);
     s.c = 127.0f * p;
-    s.m = amax * p;
-    s.r = __frcp_rn(s.m);
-    s.scale = __fdiv_rn(amax, 127.0f);
+    s.m = amax_bits ? amax * p : 1.0f;   // a row of zeros: any
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.r) : "f"(s.m));
     return s;
+}
+
+// What the codes are to be multiplied by: amax / 127, 1 for a row of zeros,
+// NaN for a row with an infinity or NaN (its products come out NaN).
+template <bool HALF>
+__device__ __forceinline__ float code_scale(uint32_t amax_bits)
+{
+    if (amax_bits == 0u) return 1.0f;
+    if (amax_bits >= (HALF ? 0x7C00u : 0x7F80u)) return __uint_as_float(0x7FC00000u);
+    return __fdiv_rn(widen<HALF>(amax_bits), 127.0f);
 }
 
 // Two FP32 operations in one instruction (each rounded as its scalar form).
@@ -140,7 +138,7 @@ __device__ __forceinline__ uint2 codes8(uint4 v, const RowScale& s, bool finite)
 }
 
 // Elements [k, k + 8) of a row of `cols`; nothing behind the row is read.
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t k, int64_t cols)
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int cols)
 {
     if (k + 8 <= cols) return qdev::ld_stream(reinterpret_cast<const uint4*>(row + k));
     uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -150,7 +148,7 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t k, int64_t c
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void store8(int8_t* row, int64_t k, int64_t cols, uint2 q)
+__device__ __forceinline__ void store8(int8_t* row, int k, int cols, uint2 q)
 {
     if (k + 8 <= cols) {
         *reinterpret_cast<uint2*>(row + k) = q;
@@ -161,9 +159,23 @@ __device__ __forceinline__ void store8(int8_t* row, int64_t k, int64_t cols, uin
         if (k + i < cols) row[k + i] = (int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
 }
 
+// Largest magnitudes of two pairs of 16-bit floats, NaN where either has one
+// (the sign of the result says nothing).
+template <bool HALF>
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if (HALF)
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 struct QuantArgs {
     const uint16_t* x;
-    int64_t rows_in, cols, ld;
+    int64_t rows_in, ld;
+    int cols;
     const int32_t* index;   // source row of each output row, or NULL
     int64_t rows;
     int8_t* codes;
@@ -173,7 +185,8 @@ struct QuantArgs {
 
 // TPR threads a row (32: a warp, several rows a block; else the block),
 // CH 8-element chunks a thread; CH = 0: rows of any length, read twice.
-template <bool HALF, int TPR, int CH, int THREADS>
+// FULL: a row is exactly TPR * CH * 8 elements.
+template <bool HALF, int TPR, int CH, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const QuantArgs p)
 {
     // The next kernel may start its set-up; this one starts before the one
@@ -187,26 +200,31 @@ __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const QuantArgs 
     int64_t src = row;
     bool inside = have;
     if (p.index && have) {
-        src = __ldg(p.index + row);
+        src = __ldcg(p.index + row);   // (the kernel before may have written it)
         inside = src >= 0 && src < p.rows_in;   // an index outside gives a row of zeros
     }
     if (!inside) src = 0;
     const uint16_t* x = p.x + src * p.ld;
-    const int64_t cols = inside ? p.cols : 0;
+    const int cols = inside ? p.cols : 0;
     uint4 v[CH > 0 ? CH : 1];
-    uint32_t amax = 0;
+    uint32_t top = 0;   // the magnitudes of even and odd elements
+    auto raise = [&](uint4 u) { top = absmax2<HALF>(top, absmax2<HALF>(absmax2<HALF>(u.x, u.y), absmax2<HALF>(u.z, u.w))); };
     if (CH > 0) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int64_t k = ((int64_t)c * TPR + t) * 8;
-            v[c] = k < cols ? load8(x, k, cols) : make_uint4(0u, 0u, 0u, 0u);
+            const int k = (c * TPR + t) * 8;
+            if (FULL && inside)
+                v[c] = qdev::ld_stream(reinterpret_cast<const uint4*>(x + k));
+            else
+                v[c] = !FULL && k < cols ? load8(x, k, cols) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int c = 0; c < CH; ++c) amax = max(amax, qdev::absmax8(v[c]));
+        for (int c = 0; c < CH; ++c) raise(v[c]);
     } else {
-        for (int64_t k = t * 8; k < cols; k += TPR * 8) amax = max(amax, qdev::absmax8(load8(x, k, cols)));
+        for (int k = t * 8; k < cols; k += TPR * 8) raise(load8(x, k, cols));
     }
-    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    top &= 0x7FFF7FFFu;
+    uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
     if (TPR > 32) {
         __shared__ uint32_t part[ROWS][TPR / 32];
         if ((t & 31) == 0) part[threadIdx.x / TPR][t >> 5] = amax;
@@ -215,25 +233,28 @@ __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const QuantArgs 
         for (int i = 0; i < TPR / 32; ++i) amax = max(amax, part[threadIdx.x / TPR][i]);
     }
     if (!have) return;
-    const RowScale s = row_scale<HALF>(amax);
     const bool finite = amax < (HALF ? 0x7C00u : 0x7F80u);
-    if (t == 0) p.scales[row] = s.scale;
+    const RowScale s = row_scale<HALF>(finite ? amax : 0u);
+    if (t == 0) p.scales[row] = code_scale<HALF>(amax);
     int8_t* out = p.codes + row * p.ldc;
     if (CH > 0) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int64_t k = ((int64_t)c * TPR + t) * 8;
-            if (k < p.cols) store8(out, k, p.cols, codes8<HALF>(v[c], s, finite));
+            const int k = (c * TPR + t) * 8;
+            if (FULL)
+                *reinterpret_cast<uint2*>(out + k) = codes8<HALF>(v[c], s, finite);
+            else if (k < p.cols)
+                store8(out, k, p.cols, codes8<HALF>(v[c], s, finite));
         }
     } else {
-        for (int64_t k = t * 8; k < p.cols; k += TPR * 8)
+        for (int k = t * 8; k < p.cols; k += TPR * 8)
             store8(out, k, p.cols,
                    codes8<HALF>(k < cols ? load8(x, k, cols) : make_uint4(0u, 0u, 0u, 0u), s, finite));
     }
 }
 
-template <bool HALF, int TPR, int CH, int THREADS>
-cudaError_t launch(const QuantArgs& p, cudaStream_t s)
+template <bool HALF, int TPR, int CH, int THREADS, bool FULL>
+cudaError_t launch_kernel(const QuantArgs& p, cudaStream_t s)
 {
     constexpr int ROWS = THREADS / TPR;
     cudaLaunchConfig_t cfg = {};
@@ -245,16 +266,29 @@ cudaError_t launch(const QuantArgs& p, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quantize_int8_kernel<HALF, TPR, CH, THREADS>, p);
+    return cudaLaunchKernelEx(&cfg, quantize_int8_kernel<HALF, TPR, CH, THREADS, FULL>, p);
+}
+
+template <bool HALF, int TPR, int CH, int THREADS>
+cudaError_t launch(const QuantArgs& p, cudaStream_t s)
+{
+    if (CH > 0 && p.cols == TPR * CH * 8) return launch_kernel<HALF, TPR, CH, THREADS, CH != 0>(p, s);
+    return launch_kernel<HALF, TPR, CH, THREADS, false>(p, s);
 }
 
 template <bool HALF>
 cudaError_t dispatch(const QuantArgs& p, cudaStream_t s)
 {
+    // A warp a row while it holds it: 16384 rows of 2048 18.4 us, 19.8 with a
+    // block of 128 threads a row.
     if (p.cols <= 256) return launch<HALF, 32, 1, 128>(p, s);
     if (p.cols <= 512) return launch<HALF, 32, 2, 128>(p, s);
     if (p.cols <= 1024) return launch<HALF, 32, 4, 128>(p, s);
     if (p.cols <= 2048) return launch<HALF, 32, 8, 128>(p, s);
+    // Then a block a row.  Many rows: more chunks a thread, so that more bytes
+    // are in flight (8192 rows of 8192: 8 chunks 33.2, 4 33.9, 2 42.3 us; 8194
+    // of 4096: 4 17.8, 2 20.9).  Few: more threads (one row of 4096: 2 chunks
+    // 1.8, 4 2.1, 8 2.5 us; of 8192: 4 chunks 2.1, 8 2.6).
     const bool many = p.rows > 1024;
     if (p.cols <= 4096) return many ? launch<HALF, 128, 4, 128>(p, s) : launch<HALF, 256, 2, 256>(p, s);
     if (p.cols <= 8192) return many ? launch<HALF, 128, 8, 128>(p, s) : launch<HALF, 256, 4, 256>(p, s);
@@ -269,7 +303,7 @@ cudaError_t launch_quantize_int8(int dtype, const uint16_t* x, int64_t rows_in, 
                                  const int32_t* row_index, int64_t rows, int8_t* codes, int64_t ldc,
                                  float* scales, cudaStream_t s)
 {
-    const QuantArgs p = {x, rows_in, cols, ld, row_index, rows, codes, ldc, scales};
+    const QuantArgs p = {x, rows_in, ld, (int)cols, row_index, rows, codes, ldc, scales};
     const cudaError_t e = dtype == FP4_FP16 ? dispatch<true>(p, s) : dispatch<false>(p, s);
     if (e != cudaSuccess) set_last_error("INT8 quantizer launch", e);
     return e;
