@@ -7,12 +7,13 @@
 // and the result is rounded once, to BF16 or FP16.
 //
 // Two kernels:
-//   int8_pair_kernel   many tokens: persistent CTA pairs, 256 x 256 (or
-//                      256 x 128) tiles.  Bound by the tensor pipe.
-//   int8_swap_kernel   few tokens: the weights on the 128-row MMA side, 16 to
-//                      128 tokens on the other, K split over a cluster whose
-//                      CTAs join their sums through distributed shared
-//                      memory.  Bound by HBM (the weights are read once).
+//   int8_pair_kernel   many tokens: persistent CTA pairs, tiles of 256
+//                      channels x 32 to 256 tokens.  Bound by the tensor pipe.
+//   int8_swap_kernel   few tokens: tiles of 128 channels x 16 to 128 tokens,
+//                      K split over a cluster whose CTAs join their sums
+//                      through distributed shared memory.  Bound by HBM (the
+//                      weights are read once).
+// Both have the weights on the MMA's fixed side and the tokens on the other.
 // Scales, bias and offsets are read past L1 (they may be written by the kernel
 // before, which can still be running when these kernels start).
 // Both take a grouped launch's tile list from the offsets themselves, so a
@@ -52,11 +53,10 @@ struct I8Params {
     int64_t ldd;
     int32_t M, N;            // rows of A and D, output channels
     int32_t ks_total;        // stages of a tile (0: K = 0, the sums are zero)
-    int32_t tiles_n;
-    // pair kernel: tile width and its stages, whether a partial last wave may
-    // be halved, M tiles per group of the tile order
-    int32_t bn, stages, halves;
-    int32_t raster_gm;
+    int32_t tiles_n;         // channel tiles
+    // pair kernel: most tokens of a tile and the stages that fit, token tiles
+    // per group of the tile order
+    int32_t bt, stages, raster_gm;
     int32_t E;               // experts (dense: 1)
     const int32_t* offsets;  // [E + 1] (dense: NULL, one group of all M rows)
     int32_t b_static;        // B is not written by the previous kernel
@@ -123,25 +123,6 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr)
                  : "r"(cluster_addr)
                  : "memory");
     return v;
-}
-
-// One step of a 4 x 4 transposition of 16-byte pieces (v[4 j .. 4 j + 3] is
-// piece j) among the lanes of a quad: pieces and lanes whose numbers differ in
-// bit `bit` (1 or 2) change places.
-__device__ __forceinline__ void quad_transpose(uint32_t (&v)[16], int lane, int bit)
-{
-    const bool upper = lane & bit;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j & bit) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t &lo = v[4 * j + i], &hi = v[4 * (j | bit) + i];
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? lo : hi, bit);
-            if (upper) lo = got;
-            else hi = got;
-        }
-    }
 }
 
 template <bool HALF>
@@ -514,11 +495,14 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 }
 
 // ------------------------------------------------------------------------
-// Many tokens: a cluster of two CTAs computes a 256 x bn tile with pair MMAs
-// (M = 256, N = bn, a multiple of 32 up to 256 that the host chooses): each
-// CTA stages its own 128 rows of A and half of the tile's B rows.  Two
-// accumulators in tensor memory, so that a tile's epilogue runs beside the
-// next tile's MMAs.
+// Many tokens: a cluster of two CTAs computes 256 channels of up to bt tokens
+// with pair MMAs (M = 256 channels, N = a multiple of 32 tokens up to 256):
+// each CTA stages its own 128 rows of weights and half of the tile's tokens.
+// The weights are on the MMA's fixed side, so that a group's last tile can be
+// as narrow as its rows: 8192 rows over 8 experts of 14336x4096 332 us, 352
+// with the tokens on that side; 7104 over 64 of 6103x1024 85 against 110 us;
+// one group of whole tiles the same within 3 %.  Two accumulators in tensor memory, so that a
+// tile's epilogue runs beside the next tile's MMAs.
 //   warp 0      producer (both CTAs; loads complete on the leader's full[s])
 //   warp 1      MMA issue (leader): passes a stage's named barrier, issues
 //               four MMAs and the commit that releases the stage in both
@@ -527,41 +511,48 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 //   warp 2      gatekeeper (leader): waits for the accumulator's release and
 //               for each stage, then opens the stage's named barrier
 //   warp 3      grouped: the tile list from the offsets
-//   warps 4-11  epilogue: two warps a tensor-memory lane quadrant, 32 columns
-//               in turn; scales, bias, 16 bits, and from the registers to D,
-//               four lanes a row (sixteen warps were 10 % faster where the
-//               sums are short, K = 128 to 512, and 0.5 us slower a launch)
+//   warps 4-11  epilogue: two warps a tensor-memory lane quadrant (32
+//               channels), 32 tokens in turn; scaled, rounded, turned into
+//               rows through the warp's block of shared memory, stored four
+//               lanes a row
 // Every wait is bounded; a CTA that gives up records it in the error word.
 // ------------------------------------------------------------------------
 constexpr int kI8EpiWarps = 8;
-constexpr int kI8Parts = kI8EpiWarps / 4;        // epilogue warps a tensor-memory lane quadrant
-constexpr int kI8Chunks = 256 / 32 / kI8Parts;   // 32-column chunks of each
 constexpr int kI8PairThreads = 128 + 32 * kI8EpiWarps;
 constexpr int kI8PairMaxStages = 12;
 
 struct I8Pair {
-    static constexpr int OFF_SCALE = 0;                                            // sB and bias of a warp's columns
-    static constexpr int OFF_LIST = OFF_SCALE + 4 * 2 * 256 * 4;          // experts' first tiles and bounds
+    static constexpr int OFF_EPI = 0;                                         // a warp's 32 tokens x 32 channels of results
+    static constexpr int OFF_SA = OFF_EPI + kI8EpiWarps * 32 * 32 * 2;        // sA of a warp's tokens
+    static constexpr int OFF_LIST = OFF_SA + kI8EpiWarps * 128 * 4;           // experts' first tiles and rows
     static constexpr int OFF_BARS = OFF_LIST + 2 * (kMaxExperts + 2) * 4;
     static constexpr int NBARS = 2 * kI8PairMaxStages + 5;
-    static constexpr int FIXED = (OFF_BARS + 256 + 1023) / 1024 * 1024;            // what lies before the stages
+    static constexpr int FIXED = (OFF_BARS + 256 + 1023) / 1024 * 1024;       // what lies before the stages
     static constexpr int SMEM = 232448;
     static constexpr int STAGE_ROOM = SMEM - 1024 - FIXED;
     static_assert(NBARS * 8 + 8 <= 256, "barrier area");
     static_assert(OFF_BARS % 16 == 0, "barrier alignment");
     static_assert(kI8PairMaxStages + 1 <= 16, "one named barrier per stage (ids from 1)");
-    __host__ __device__ static constexpr int stage_bytes(int bn) { return I8_TILE + bn / 2 * I8_BK; }
-    static constexpr int stages(int bn)
+    static_assert(STAGE_ROOM >= 6 * (I8_TILE + 128 * I8_BK), "six stages of the widest tile");
+    // a CTA's share of a stage with `width` tokens
+    __host__ __device__ static constexpr int stage_bytes(int width) { return I8_TILE + width / 2 * I8_BK; }
+    static constexpr int stages(int bt)
     {
-        const int n = STAGE_ROOM / stage_bytes(bn);
+        const int n = STAGE_ROOM / stage_bytes(bt);
         return n < kI8PairMaxStages ? n : kI8PairMaxStages;
     }
 };
 
+// The tokens with boxes of one to four quarters of a CTA's share of the widest
+// tile: a narrower tile is loaded by the smallest that holds it, in one piece
+// (pieces of 16 rows cost more: a tile half as wide 18.6 instead of 12.3 us).
+struct TokenMaps {
+    CUtensorMap q[4];
+};
+
 template <bool HALF, bool GROUPED>
 __global__ void __launch_bounds__(kI8PairThreads, 1)
-int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmBh, const I8Params p)
+int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ TokenMaps tmX, const I8Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -578,7 +569,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
     const int stages = p.stages;
-    const uint32_t stage_bytes = (uint32_t)I8Pair::stage_bytes(p.bn);
+    const uint32_t stage_bytes = (uint32_t)I8Pair::stage_bytes(p.bt);
     const uint32_t smem0 = smem_u32(smem) + I8Pair::FIXED;   // first stage
     const uint32_t bar0 = smem_u32(bars);
     auto FULL = [&](int s) { return bar0 + 8u * s; };
@@ -614,7 +605,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             int first, end;
             expert_bounds(p, e0, lane, reached, first, end);
-            const int tiles = (end - first + 255) / 256 * p.tiles_n;
+            const int tiles = (end - first + p.bt - 1) / p.bt * p.tiles_n;
             const int upto = warp_scan_add(tiles, lane);
             if (e0 + lane < p.E) {
                 list[e0 + lane] = seen + upto - tiles;
@@ -634,27 +625,27 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     const int pair = blockIdx.x >> 1;
     const int npairs = gridDim.x >> 1;
-    const int tiles = GROUPED ? list[p.E] : (p.M + 255) / 256 * p.tiles_n;
+    const int tiles = GROUPED ? list[p.E] : (p.M + p.bt - 1) / p.bt * p.tiles_n;
     // Work items: the tiles, dealt round-robin.  A last, partial wave whose
-    // halves fit on the pairs is computed as halves of bn / 2 columns.
+    // halves fit on the pairs is computed as halves, of the tokens.
     const int rem = tiles % npairs;
-    const int split_from = p.halves && 2 * rem <= npairs ? tiles - rem : tiles;
+    const int split_from = 2 * rem <= npairs ? tiles - rem : tiles;
     const int items = 2 * tiles - split_from;
-    // Expert, first row and channel of item t, its width, and the end of the
-    // expert's rows.  Within an expert groups of raster_gm consecutive M
-    // tiles sweep the N tiles together (M fastest), so that a group's A rows
-    // stay in L2 while B streams past them once.
+    // Expert, first token, first channel and width (tokens rounded up to 32;
+    // 0: nothing to do) of item t, and the end of the expert's rows.  Within
+    // an expert groups of raster_gm consecutive token tiles sweep the channel
+    // tiles together (token tiles fastest), so that a group's tokens stay in
+    // L2 while the weights stream past them once.
     struct Place {
         int e, row, col, width, row_end;
     };
     auto locate = [&](int t) {
         Place w;
         int half = 0;
-        w.width = p.bn;
-        if (t >= split_from) {
+        const bool halved = t >= split_from;
+        if (halved) {
             half = (t - split_from) & 1;
             t = split_from + ((t - split_from) >> 1);
-            w.width = p.bn / 2;
         }
         int lo = 0, base = 0, end = p.M;
         if (GROUPED) {
@@ -670,28 +661,33 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             // rows end where the next expert's begin
             end = bound[lo + 1];
         }
-        const int tiles_m = (end - base + 255) >> 8;
+        const int tiles_m = (end - base + p.bt - 1) / p.bt;
         const int span = p.raster_gm * p.tiles_n;
         const int grp = t / span, in = t - grp * span;
         const int m0 = grp * p.raster_gm;
         const int gm = min(tiles_m - m0, p.raster_gm);
         w.e = lo;
-        w.row = base + (m0 + in % gm) * 256;
-        w.col = in / gm * p.bn + half * w.width;
+        w.row = base + (m0 + in % gm) * p.bt;
+        w.col = in / gm * 256;
+        w.width = min(p.bt, (end - w.row + 31) & ~31);
         w.row_end = end;
+        if (halved) {
+            const int upper = (w.width / 2 + 31) & ~31;   // the first half's tokens
+            w.row += half * upper;
+            w.width = half ? w.width - upper : upper;
+        }
         return w;
     };
 
     if (warp == 0) {
         if (lane == 0) {
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
-            // B rows of a stage: half of the item's columns in each CTA
-            auto load_b = [&](const Place& w, int s, int ks) {
-                if (leader) mbar_arrive_expect_tx(FULL(s), 2u * (uint32_t)I8Pair::stage_bytes(w.width));
-                const int y = w.col + (int)rank * (w.width / 2);
-                tma_load_3d_pair(w.width == p.bn ? &tmB : &tmBh, map_to_rank(FULL(s), 0),
-                                 smem0 + s * stage_bytes + I8_TILE, ks * I8_BK, y, w.e);
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmX.q[3])) : "memory");
+            auto box = [&](const Place& w) { return (w.width * 4 + p.bt - 1) / p.bt; };   // quarters
+            auto load_w = [&](const Place& w, int s, int ks) {
+                if (leader) mbar_arrive_expect_tx(FULL(s), 2u * (I8_TILE + box(w) * (p.bt / 8) * I8_BK));
+                tma_load_3d_pair(&tmW, map_to_rank(FULL(s), 0), smem0 + s * stage_bytes, ks * I8_BK,
+                                 w.col + (int)rank * I8_BM, w.e);
             };
             int stage = 0, pre = 0;
             uint32_t phase = 0;
@@ -700,23 +696,27 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 // static weights: those of the first stages are requested
                 // before the dependency wait
                 const Place w = locate(pair);
-                for (; pre < stages && pre < p.ks_total; ++pre) load_b(w, pre, pre);
+                if (w.width > 0)
+                    for (; pre < stages && pre < p.ks_total; ++pre) load_w(w, pre, pre);
             }
             pdl_wait();
             for (int t = pair; ok && t < items; t += npairs) {
                 const Place w = locate(t);
-                const int ya = w.row + (int)rank * I8_BM;
+                if (w.width == 0) continue;
+                const CUtensorMap* map = &tmX.q[box(w) - 1];
+                const int y = w.row + (int)rank * (w.width / 2);   // this CTA's half of the tokens
                 for (int ks = 0; ks < p.ks_total; ++ks) {
                     if (pre > 0) {
-                        --pre;   // this stage's B tile is on its way
+                        --pre;   // this stage's weights are on their way
                     } else {
                         if (!wait_fast(EMPTY(stage), phase ^ 1u, abort_flag, ERR_EMPTY)) {
                             ok = false;
                             break;
                         }
-                        load_b(w, stage, ks);
+                        load_w(w, stage, ks);
                     }
-                    tma_load_3d_pair(&tmA, map_to_rank(FULL(stage), 0), smem0 + stage * stage_bytes, ks * I8_BK, ya, 0);
+                    tma_load_3d_pair(map, map_to_rank(FULL(stage), 0), smem0 + stage * stage_bytes + I8_TILE, ks * I8_BK, y,
+                                     0);
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
@@ -733,8 +733,10 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint64_t bdesc0 = desc_sw128(smem0 + I8_TILE);
             int stage = 0, buf = 0;
             for (int t = pair; t < items; t += npairs) {
+                const int width = locate(t).width;
+                if (width == 0) continue;
                 const uint32_t acc = tmem_base + (uint32_t)(buf * 256);
-                const uint32_t idesc = idesc_i8(256, t >= split_from ? p.bn / 2 : p.bn);
+                const uint32_t idesc = idesc_i8(256, width);
                 for (int ks = 0; ks < p.ks_total; ++ks) {
                     named_bar_sync(1 + stage, 64);
                     if (lane == 0) {
@@ -769,6 +771,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int t = pair; t < items; t += npairs) {
+                if (locate(t).width == 0) continue;
                 if (ok && !warp_wait(ACC_EMPTY(buf), acc_phase ^ 1u, abort_flag, ERR_ACC_EMPTY)) ok = false;
                 for (int ks = 0; ks < p.ks_total; ++ks) {
                     if (ok && !warp_wait(FULL(stage), phase, abort_flag, ERR_FULL)) ok = false;
@@ -784,26 +787,25 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp >= 4) {
         const int q = warp & 3;                  // tensor-memory lane quadrant
-        const int part = (warp - 4) >> 2;        // the warp's 32-column chunks: part, part + kI8Parts, ...
-        float* sbs = reinterpret_cast<float*>(smem + I8Pair::OFF_SCALE) + (warp - 4) * (2 * 32 * kI8Chunks);
-        float* bis = sbs + 32 * kI8Chunks;
+        const int half = (warp - 4) >> 2;        // the warp's 32-token chunks: half, half + 2, ...
+        float* sas = reinterpret_cast<float*>(smem + I8Pair::OFF_SA) + (warp - 4) * 128;
+        const uint32_t blk = smem_u32(smem) + I8Pair::OFF_EPI + (warp - 4) * (32 * 32 * 2);
         pdl_wait();
-        // The scales of an item (this lane's row, a column of each chunk) are
-        // read while the item before it is worked on.
+        // The scales of an item (this lane's channel, a token of each chunk)
+        // are read while the item before it is worked on.
         Place next = {};
-        float sa_next = 0.0f, sb_next[kI8Chunks] = {}, bias_next[kI8Chunks] = {};
+        float sb_next = 0.0f, bias_next = 0.0f, sa_next[4] = {};
         auto fetch = [&](int t) {
             if (t >= items) return;
             next = locate(t);
-            const int y = next.row + (int)rank * I8_BM + q * 32 + lane;
-            if (y < next.row_end) sa_next = __ldcg(p.sa + y);
-            const int64_t chan_base = (int64_t)next.e * p.N;
+            const int n = next.col + (int)rank * I8_BM + q * 32 + lane;
+            const int64_t chan = (int64_t)next.e * p.N + n;
+            sb_next = n < p.N ? __ldcg(p.sb + chan) : 0.0f;
+            bias_next = n < p.N && p.bias ? __ldcg(p.bias + chan) : 0.0f;
 #pragma unroll
-            for (int c = 0; c < kI8Chunks; ++c) {
-                const int n = next.col + (part + kI8Parts * c) * 32 + lane;
-                const bool in = (part + kI8Parts * c) * 32 < next.width && n < p.N;
-                sb_next[c] = in ? __ldcg(p.sb + chan_base + n) : 0.0f;
-                bias_next[c] = in && p.bias ? __ldcg(p.bias + chan_base + n) : 0.0f;
+            for (int c = 0; c < 4; ++c) {
+                const int y = next.row + (half + 2 * c) * 32 + lane;
+                sa_next[c] = (half + 2 * c) * 32 < next.width && y < next.row_end ? __ldcg(p.sa + y) : 0.0f;
             }
         };
         fetch(pair);
@@ -811,27 +813,26 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         int buf = 0;
         for (int t = pair; t < items; t += npairs) {
             const Place w = next;
-            const float sa = sa_next;
+            const float sb = sb_next, bias = bias_next;
+            __syncwarp();   // the scales' memory has been read
 #pragma unroll
-            for (int c = 0; c < kI8Chunks; ++c) {
-                sbs[c * 32 + lane] = sb_next[c];
-                bis[c * 32 + lane] = bias_next[c];
-            }
+            for (int c = 0; c < 4; ++c) sas[c * 32 + lane] = sa_next[c];
             __syncwarp();
             fetch(t + npairs);
-            const int y0 = w.row + (int)rank * I8_BM + q * 32;
-            const int chunks = (w.width / 32 - part + kI8Parts - 1) / kI8Parts;   // 0 to kI8Chunks
+            if (w.width == 0) continue;
+            const int chunks = (w.width / 32 - half + 1) >> 1;   // 0 to 4
+            const int x0 = w.col + (int)rank * I8_BM + q * 32;   // the warp's first channel
             if (!warp_wait(ACC_FULL(buf), acc_phase, abort_flag, ERR_ACC_FULL)) break;
             tc_fence_after();
-            const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 256 + part * 32);
+            const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * 256 + half * 32);
             uint32_t r2[2][32];
             if (chunks > 0) tmem_ld32(trow, r2[0]);
 #pragma unroll
-            for (int c = 0; c < kI8Chunks; ++c) {
+            for (int c = 0; c < 4; ++c) {
                 uint32_t (&r)[32] = r2[c & 1];
                 if (c < chunks) tmem_wait_ld(r);
                 if (c + 1 < chunks) {   // the next chunk's load overlaps this one's arithmetic
-                    tmem_ld32(trow + (uint32_t)((c + 1) * kI8Parts * 32), r2[(c + 1) & 1]);
+                    tmem_ld32(trow + (uint32_t)((c + 1) * 64), r2[(c + 1) & 1]);
                 } else if (c == max(chunks - 1, 0)) {
                     // every column is in registers: hand the accumulator back
                     tc_fence_before();
@@ -843,38 +844,44 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             mbar_arrive_cluster_relaxed(map_to_rank(ACC_EMPTY(buf), 0));
                     }
                 }
-                const int x0 = w.col + (part + kI8Parts * c) * 32;
+                const int y0 = w.row + (half + 2 * c) * 32;
                 if (c < chunks && y0 < w.row_end && x0 < p.N) {
-                    uint32_t v[16];
+                    // 32 tokens x 32 channels of results: token i's in row i
+                    // (64 bytes), whose 16-byte pieces are rotated so that the
+                    // reads below are free of bank conflicts
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 s4 = *reinterpret_cast<const float4*>(sbs + c * 32 + 4 * i);
-                        const float4 b4 = *reinterpret_cast<const float4*>(bis + c * 32 + 4 * i);
-                        v[2 * i] = pack16<HALF>(scaled((int)r[4 * i], sa, s4.x, b4.x),
-                                                scaled((int)r[4 * i + 1], sa, s4.y, b4.y));
-                        v[2 * i + 1] = pack16<HALF>(scaled((int)r[4 * i + 2], sa, s4.z, b4.z),
-                                                    scaled((int)r[4 * i + 3], sa, s4.w, b4.w));
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 sa = *reinterpret_cast<const float4*>(sas + c * 32 + i);
+                        const uint32_t lo = pack16<HALF>(scaled((int)r[i], sa.x, sb, bias), scaled((int)r[i + 1], sa.y, sb, bias));
+                        const uint32_t hi = pack16<HALF>(scaled((int)r[i + 2], sa.z, sb, bias), scaled((int)r[i + 3], sa.w, sb, bias));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t v = k < 2 ? lo : hi;
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(
+                                             blk + (i + k) * 64 + (((lane >> 3) ^ (((i + k) >> 1) & 3)) << 4) + 2 * (lane & 7)),
+                                         "h"((uint16_t)(k & 1 ? v >> 16 : v))
+                                         : "memory");
+                        }
                     }
-                    // Four lanes exchange their rows' 16-byte pieces, so that
-                    // lane i has piece i of all four rows and they store 64
-                    // bytes of one row at a time.
-                    quad_transpose(v, lane, 1);
-                    quad_transpose(v, lane, 2);
-                    const int x = x0 + 8 * (lane & 3);
-                    uint16_t* d = p.D + (int64_t)(y0 + (lane & 28)) * p.ldd + x;
+                    __syncwarp();
+                    const int x = x0 + 8 * (lane & 3);   // four lanes a token
 #pragma unroll
-                    for (int k = 0; k < 4; ++k, d += p.ldd) {
-                        if (y0 + (lane & 28) + k >= w.row_end) break;   // the next expert's row, or none
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = 8 * k + (lane >> 2);
+                        const uint4 v = ld_shared_v4(blk + i * 64 + (((lane & 3) ^ ((i >> 1) & 3)) << 4));
+                        if (y0 + i >= w.row_end) break;   // the next expert's row, or none
+                        uint16_t* d = p.D + (int64_t)(y0 + i) * p.ldd + x;
                         if (x + 8 <= p.N) {
-                            *reinterpret_cast<uint4*>(d) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                            *reinterpret_cast<uint4*>(d) = v;
                         } else {
+                            const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (x + i < p.N) d[i] = (uint16_t)(v[4 * k + (i >> 1)] >> (16 * (i & 1)));
+                            for (int j = 0; j < 8; ++j)
+                                if (x + j < p.N) d[j] = (uint16_t)(word[j >> 1] >> (16 * (j & 1)));
                         }
                     }
                 }
-                __syncwarp();   // (after the last chunk: the scales' memory is written again)
             }
             buf ^= 1;
             if (buf == 0) acc_phase ^= 1u;
@@ -965,9 +972,8 @@ I8Params params_of(const Int8GemmArgs& a, int bn)
     p.N = (int32_t)a.N;
     p.ks_total = (int32_t)((a.K + I8_BK - 1) / I8_BK);
     p.tiles_n = (int32_t)((a.N + bn - 1) / bn);
-    p.bn = bn;
+    p.bt = 0;
     p.stages = 0;
-    p.halves = 0;
     p.raster_gm = 1;
     p.E = (int32_t)a.E;
     p.offsets = a.offsets;
@@ -1001,24 +1007,26 @@ cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, int 
 }
 
 template <bool HALF, bool GROUPED>
-cudaError_t launch_pair(const Int8GemmArgs& a, int bn, int64_t tiles, int sm_count, cudaStream_t s)
+cudaError_t launch_pair(const Int8GemmArgs& a, int bt, int64_t tiles, int sm_count, cudaStream_t s)
 {
-    I8Params p = params_of(a, bn);
-    p.stages = I8Pair::stages(bn);
-    const int64_t pairs = sm_count / 2;
-    const int64_t grid = tiles < pairs ? tiles : pairs;
-    // halves are multiples of 32 columns
-    p.halves = bn % 64 == 0 && (GROUPED || 2 * (tiles % grid) <= grid);
-    CUtensorMap ta, tb, tbh = {};
-    if (!make_map_i8(&ta, a.A, 1, a.M, a.K, a.lda, a.lda, I8_BM) ||
-        !make_map_i8(&tb, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, bn / 2) ||
-        (p.halves && !make_map_i8(&tbh, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, bn / 4))) {
+    I8Params p = params_of(a, 256);
+    p.bt = bt;
+    p.stages = I8Pair::stages(bt);
+    const int64_t pairs = sm_count / 2, grid = tiles < pairs ? tiles : pairs;
+    CUtensorMap tw;
+    TokenMaps tx = {};
+    // only the whole box where every tile is whole
+    const bool narrow = GROUPED || a.M % bt != 0 || 2 * (tiles % grid) <= grid;
+    bool ok = make_map_i8(&tw, a.B, a.E, a.N, a.K, a.ldb, a.stride_b, I8_BM);
+    for (int q = narrow ? 1 : 4; q <= 4; ++q)
+        ok = ok && make_map_i8(&tx.q[q - 1], a.A, 1, a.M, a.K, a.lda, a.lda, bt / 8 * q);
+    if (!ok) {
         set_last_error("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
         return cudaErrorInvalidValue;
     }
-    // M tiles per group: as many as hold kI8GroupBytes of A, all of them when
-    // A fits in half of the L2 cache
-    const int64_t tile_bytes = 256 * a.K, tiles_m = (a.M + 255) / 256;
+    // token tiles per group: as many as hold kI8GroupBytes of A, all of them
+    // when A fits in half of the L2 cache
+    const int64_t tile_bytes = bt * a.K, tiles_m = (a.M + bt - 1) / bt;
     int64_t rg = tiles_m;
     if (tile_bytes * tiles_m > 2 * kI8GroupBytes) rg = (kI8GroupBytes + tile_bytes / 2) / tile_bytes;
     p.raster_gm = (int32_t)(rg < 1 ? 1 : rg > tiles_m ? tiles_m : rg);
@@ -1029,7 +1037,7 @@ cudaError_t launch_pair(const Int8GemmArgs& a, int bn, int64_t tiles, int sm_cou
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         launch_config(cfg, attr, 2u * (unsigned)grid, kI8PairThreads, 2, I8Pair::SMEM, s);
-        e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tbh, p);
+        e = cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
     }
     if (e != cudaSuccess) set_last_error("INT8 GEMM launch (CTA pairs)", e);
     return e;
@@ -1042,13 +1050,13 @@ cudaError_t launch_swap_t(const Int8GemmArgs& a, int split, int64_t clusters, in
                       : launch_swap<NT, false>(a, split, clusters, sm_count, s);
 }
 
-cudaError_t launch_pair_t(const Int8GemmArgs& a, int bn, int64_t tiles, int sm_count, cudaStream_t s)
+cudaError_t launch_pair_t(const Int8GemmArgs& a, int bt, int64_t tiles, int sm_count, cudaStream_t s)
 {
     if (a.offsets)
-        return a.half_out ? launch_pair<true, true>(a, bn, tiles, sm_count, s)
-                          : launch_pair<false, true>(a, bn, tiles, sm_count, s);
-    return a.half_out ? launch_pair<true, false>(a, bn, tiles, sm_count, s)
-                      : launch_pair<false, false>(a, bn, tiles, sm_count, s);
+        return a.half_out ? launch_pair<true, true>(a, bt, tiles, sm_count, s)
+                          : launch_pair<false, true>(a, bt, tiles, sm_count, s);
+    return a.half_out ? launch_pair<true, false>(a, bt, tiles, sm_count, s)
+                      : launch_pair<false, false>(a, bt, tiles, sm_count, s);
 }
 
 // Token tiles of `nt` rows that a launch may need: a grouped one knows only
@@ -1083,69 +1091,88 @@ double swap_us(int nt, int split, double tiles, int64_t ks, int sm_count)
     return 1.15 * n / resident * (fixed + kb / std::fmin(ring_kb / 1.3, 107.0 / resident));
 }
 
-// Many tokens: tiles of 256 tokens x bn channels on the CTA pairs.  A stage
-// takes 0.53 ns x (400 + bn): the tensor pipe's time is proportional to bn,
-// the loads' is not.  301x5003x4099 (2 M tiles): bn = 256 16.5, 160 14.2,
-// 128 (two waves) 20.3 us; 1024x8192x8192: 256 48.9, 224 46.3, 192 63 us.
-double pair_us(int bn, double tiles_m, int64_t N, int64_t ks, int sm_count)
+// The groups of rows of a launch, as far as the host knows them: one, or some
+// experts of which a launch knows the mean.  Experts' shares differ by several
+// times, so three sizes stand for them.
+struct Groups {
+    double count;      // groups with rows, at most
+    int kinds;
+    double rows[3], share[3];
+};
+
+Groups groups_of(const Int8GemmArgs& a)
 {
-    const double pairs = sm_count / 2;
-    const double tiles = std::ceil(tiles_m * ((N + bn - 1) / bn));
-    const double full = std::floor(tiles / pairs), rem = tiles - full * pairs;
-    double columns = full * (400 + bn);
-    if (rem > 0) columns += 400 + (full > 0 && bn % 64 == 0 && 2 * rem <= pairs ? bn / 2 : bn);
-    return 3.4 + 0.0085 * bn + 0.00053 * columns * ks;
+    if (!a.offsets) return {1, 1, {(double)a.M}, {1}};
+    const double some = (double)(a.E < a.M ? a.E : a.M), mean = a.M / some;
+    return {some, 3, {0.4 * mean, mean, 2.4 * mean}, {0.4, 0.35, 0.25}};
+}
+
+// Many tokens: tiles of 256 channels x bt tokens on the CTA pairs, the last of
+// each group as narrow as its rows allow.  A stage takes 0.53 ns x (400 +
+// width): the tensor pipe's time is proportional to the width, the loads' is
+// not.  301x5003x4099: bt = 128 14.0, 160 14.9, 256 17.1 us; 1024x8192x8192:
+// 256 49.6, 192 59.8 us; 7680 rows over 128 experts of 2283x896: 192 55.5, 256
+// 57.9, 128 62.5 us.
+double pair_us(int bt, const Groups& g, int64_t N, int64_t ks, int sm_count)
+{
+    const double pairs = sm_count / 2, tiles_n = (double)((N + 255) / 256);
+    double tiles = 0, columns = 0, widest = 0;
+    for (int i = 0; i < g.kinds; ++i) {
+        const double whole = std::floor(g.rows[i] / bt), rest = std::ceil((g.rows[i] - whole * bt) / 32) * 32;
+        tiles += g.share[i] * (whole + (rest > 0 ? 1 : 0));
+        columns += g.share[i] * (whole * (400 + bt) + (rest > 0 ? 400 + rest : 0));
+        widest = std::fmax(widest, 400 + (whole > 0 ? bt : rest));
+    }
+    tiles *= g.count * tiles_n;
+    columns *= g.count * tiles_n;
+    double longest = widest;   // of a pair
+    if (tiles > pairs) {
+        const double full = std::floor(tiles / pairs), rem = tiles - full * pairs;
+        longest = full * columns / tiles + (rem == 0 ? 0 : 2 * rem <= pairs ? 400 + bt / 2 : widest);
+    }
+    return 3.4 + 0.0085 * bt + 0.00053 * longest * ks;
 }
 
 struct Choice {
     bool swap;
-    int nt, split, bn;
+    int nt, split, bt;
 };
 
 Choice choose(const Int8GemmArgs& a, int kernel, int sm_count)
 {
     const int64_t ks = (a.K + I8_BK - 1) / I8_BK, tiles_n = (a.N + I8_BM - 1) / I8_BM;
-    const bool grouped = a.offsets != nullptr;
-    const double mean = grouped ? (double)a.M / a.E : (double)a.M;   // rows an expert
-    const double some = grouped ? (double)(a.E < a.M ? a.E : a.M) : 0;   // experts with rows, at most
-    Choice c = {true, 16, 1, 256};
+    const Groups g = groups_of(a);
+    Choice c = {true, 128, 1, 256};
     double best_swap = 1e30, best_pair = 1e30;
     for (int nt = 16; nt <= 128; nt *= 2) {
-        if (nt < 128 && 8 * nt <= mean) continue;
-        // A grouped launch knows only the mean, and experts' shares differ by
-        // several times: an expert of more than nt rows reads its weights
-        // again for each tile, so the tile is wider than the mean.  64 experts
-        // of 2056x2048, 1031 rows unevenly: 16 tokens 46.8, 64 43.1 us; 8 of
-        // 4096x4096, 256 rows: 16 tokens 32.5, 64 25.5 us; but 8 of
-        // 14336x4096, 16 rows: 16 tokens 62, 64 87 us.
-        if (grouped && nt < 64 && nt < 2 * mean && !(nt == 32 && mean <= 20)) continue;
-        if (grouped && nt > 16 && nt > 8 * mean) continue;
-        const double tiles = (grouped ? std::fmax(a.M / nt + 0.5 * some, some) : (double)((a.M + nt - 1) / nt)) * tiles_n;
+        double tiles = 0;
+        for (int i = 0; i < g.kinds; ++i) tiles += g.share[i] * std::ceil(g.rows[i] / nt);
+        tiles *= g.count * tiles_n;
         for (int split = 1; split <= 8; split *= 2) {
             if (split > 1 && (split > ks || tiles * split > swap_resident(nt) * sm_count)) break;
             const double us = swap_us(nt, split, tiles, ks, sm_count);
-            if (us < best_swap) {
+            // (a wider tile only for a clear gain: 16x4096x4096 takes 16
+            // tokens 5.4, 32 6.1 us)
+            if (us < (nt == c.nt ? 1.0 : 0.93) * best_swap) {
                 best_swap = us;
                 c.nt = nt;
                 c.split = split;
             }
         }
     }
-    // a grouped launch has half an empty tile an expert, on the average
-    const double tiles_m = grouped ? std::ceil(a.M / 256.0 + 0.5 * some) : std::ceil(a.M / 256.0);
-    for (int bn = 256; bn >= 32; bn -= 32) {
-        const double us = pair_us(bn, tiles_m, a.N, ks, sm_count);
+    for (int bt = 256; bt >= 32; bt -= 32) {
+        const double us = pair_us(bt, g, a.N, ks, sm_count);
         if (us < best_pair) {
             best_pair = us;
-            c.bn = bn;
+            c.bt = bt;
         }
     }
     // Where the weights' bytes bind, the few-token kernel reads them at 5.8
-    // TB/s or more and the pair kernel, whose tiles are partly empty then, at
-    // 5.0 (64 experts of 2056x2048, 1031 rows: 48 against 56 us).
-    const double weight_mb = 1e-6 * (grouped ? some : 1) * (double)a.N * (double)a.K;
+    // TB/s or more and the pair kernel at 5.4 (64 experts of 2056x2048, 1031
+    // rows: 48 against 52 us).
+    const double weight_mb = 1e-6 * g.count * (double)a.N * (double)a.K;
     best_swap = std::fmax(best_swap, weight_mb / 5.8 + 2);
-    best_pair = std::fmax(best_pair, weight_mb / 5.0 + 4);
+    best_pair = std::fmax(best_pair, weight_mb / 5.4 + 3);
     c.swap = kernel == FP4_GEMM_DECODE || a.K == 0 || (kernel == FP4_GEMM_AUTO && best_swap <= best_pair);
     return c;
 }
@@ -1162,7 +1189,7 @@ cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo
         if (c.nt == 64) return launch_swap_t<64>(a, c.split, clusters, dev.sm_count, s);
         return launch_swap_t<128>(a, c.split, clusters, dev.sm_count, s);
     }
-    return launch_pair_t(a, c.bn, most_token_tiles(a, 256) * ((a.N + c.bn - 1) / c.bn), dev.sm_count, s);
+    return launch_pair_t(a, c.bt, most_token_tiles(a, c.bt) * ((a.N + 255) / 256), dev.sm_count, s);
 }
 
 cudaError_t read_and_clear_int8_error_word(unsigned int* word)
