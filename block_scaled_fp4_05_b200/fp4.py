@@ -337,17 +337,11 @@ def bind_gemm_decode_dynamic(x, W, sW, gsW, D, gs_out, alpha_out, workspace, str
 _DTYPE16 = {torch.bfloat16: BF16, torch.float16: FP16}
 
 
-def _i8_stream(stream, dev):
-    """The raw handle of `stream`, or of the current stream of device `dev`
-    (without the stream object that _stream makes: 0.1 us instead of 3.4)."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-def _i8_ld(t, dim, rows, cols, unit):
-    """Leading dimension of a matrix of rows x cols, stride `dim` of t.  That
-    of a single row, or of rows without elements, is never used: it counts as
-    the next multiple of `unit`."""
-    return t.stride(dim) if rows > 1 and cols > 0 else (cols + unit - 1) // unit * unit
+# The leading dimension of a single row, or of rows without elements, is never
+# used: the functions below count it as the next multiple of 16 (8 for 16-bit
+# types) bytes.  They check a call that fits in one expression, with as few
+# tensor accesses as that takes (a call's Python part is 3 to 4 us), and leave
+# it to _i8_refuse to find what does not fit.
 
 
 def _i8_refuse(matrices, vectors):
@@ -375,17 +369,21 @@ def _quantize_int8_args(x, codes, scales, row_index, stream):
     dev = torch.cuda.current_device()
     if x.dim() == 2 and codes.dim() == 2:
         (rows_in, cols), (rows, ccols) = x.shape, codes.shape
-        # one expression for the call that fits; _i8_refuse finds what does not
+        (ld, unit), (ldc, cunit) = x.stride(), codes.stride()
         if (cols == ccols and x.dtype in _DTYPE16 and codes.dtype is torch.int8
                 and scales.dtype is torch.float32 and scales.shape == (rows,) and scales.is_contiguous()
-                and (cols <= 1 or (x.stride(1) == 1 and codes.stride(1) == 1))
+                and (unit == cunit == 1 or cols <= 1)
                 and x.get_device() == dev and codes.get_device() == dev and scales.get_device() == dev
                 and (rows_in == rows if row_index is None else
                      row_index.dtype is torch.int32 and row_index.shape == (rows,) and row_index.is_contiguous()
                      and row_index.get_device() == dev)):
-            return (x.data_ptr(), _DTYPE16[x.dtype], rows_in, cols, _i8_ld(x, 0, rows_in, cols, 8),
-                    None if row_index is None else row_index.data_ptr(), rows, codes.data_ptr(),
-                    _i8_ld(codes, 0, rows, cols, 16), scales.data_ptr(), _i8_stream(stream, dev))
+            if rows_in <= 1 or cols == 0:
+                ld = (cols + 7) // 8 * 8
+            if rows <= 1 or cols == 0:
+                ldc = (cols + 15) // 16 * 16
+            return (x.data_ptr(), _DTYPE16[x.dtype], rows_in, cols, ld,
+                    None if row_index is None else row_index.data_ptr(), rows, codes.data_ptr(), ldc,
+                    scales.data_ptr(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     rows = len(x) if row_index is None else len(row_index)
     _i8_refuse([("x", x, tuple(_DTYPE16), x.shape if x.dim() == 2 else None),
                 ("codes", codes, (torch.int8,), (rows,) + tuple(x.shape[1:]))],
@@ -409,20 +407,25 @@ def bind_quantize_int8(x, codes, scales, row_index=None, stream=None):
 
 def _gemm_int8_args(A, sA, B, sB, D, bias, kernel, stream):
     dev = torch.cuda.current_device()
-    if A.dim() == 2 and B.dim() == 2:
+    if A.dim() == 2 and B.dim() == 2 and D.dim() == 2:
         (M, K), (N, KB) = A.shape, B.shape
+        (lda, ua), (ldb, ub), (ldd, ud) = A.stride(), B.stride(), D.stride()
         if (KB == K and D.shape == (M, N)
                 and A.dtype is torch.int8 and B.dtype is torch.int8 and D.dtype in _DTYPE16
                 and sA.dtype is torch.float32 and sA.shape == (M,) and sA.is_contiguous()
                 and sB.dtype is torch.float32 and sB.shape == (N,) and sB.is_contiguous()
-                and (K <= 1 or (A.stride(1) == 1 and B.stride(1) == 1)) and (N <= 1 or D.stride(1) == 1)
+                and (ua == ub == 1 or K <= 1) and (ud == 1 or N <= 1)
                 and A.get_device() == dev and B.get_device() == dev and D.get_device() == dev
                 and sA.get_device() == dev and sB.get_device() == dev
                 and (bias is None or (bias.dtype is torch.float32 and bias.shape == (N,) and bias.is_contiguous()
                                       and bias.get_device() == dev))):
-            return (A.data_ptr(), _i8_ld(A, 0, M, K, 16), sA.data_ptr(), B.data_ptr(), _i8_ld(B, 0, N, K, 16),
-                    sB.data_ptr(), M, N, K, None if bias is None else bias.data_ptr(), _DTYPE16[D.dtype],
-                    D.data_ptr(), _i8_ld(D, 0, M, N, 8), kernel, _i8_stream(stream, dev))
+            if M <= 1 or N <= 1 or K == 0:
+                pad = (K + 15) // 16 * 16
+                lda, ldb = (pad if M <= 1 or K == 0 else lda), (pad if N <= 1 or K == 0 else ldb)
+                ldd = (N + 7) // 8 * 8 if M <= 1 or N == 0 else ldd
+            return (A.data_ptr(), lda, sA.data_ptr(), B.data_ptr(), ldb, sB.data_ptr(), M, N, K,
+                    None if bias is None else bias.data_ptr(), _DTYPE16[D.dtype], D.data_ptr(), ldd, kernel,
+                    torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     a, b = A.shape, B.shape
     _i8_refuse([("A", A, (torch.int8,), a if len(a) == 2 else None),
                 ("B", B, (torch.int8,), (b[0], a[-1]) if len(b) == 2 else None),
@@ -447,27 +450,32 @@ def bind_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
 
 def _gemm_int8_grouped_args(A, sA, B, sB, offsets, D, bias, kernel, stream):
     dev = torch.cuda.current_device()
-    if A.dim() == 2 and B.dim() == 3:
+    if A.dim() == 2 and B.dim() == 3 and D.dim() == 2:
         (T, K), (E, N, KB) = A.shape, B.shape
+        (lda, ua), (stride_b, ldb, ub), (ldd, ud) = A.stride(), B.stride(), D.stride()
         if (KB == K and D.shape == (T, N)
                 and A.dtype is torch.int8 and B.dtype is torch.int8 and D.dtype in _DTYPE16
                 and sA.dtype is torch.float32 and sA.shape == (T,) and sA.is_contiguous()
                 and sB.dtype is torch.float32 and sB.shape == (E, N) and sB.is_contiguous()
                 and offsets.dtype is torch.int32 and offsets.shape == (E + 1,) and offsets.is_contiguous()
-                and (K <= 1 or (A.stride(1) == 1 and B.stride(2) == 1)) and (N <= 1 or D.stride(1) == 1)
+                and (ua == ub == 1 or K <= 1) and (ud == 1 or N <= 1)
                 and A.get_device() == dev and B.get_device() == dev and D.get_device() == dev
                 and sA.get_device() == dev and sB.get_device() == dev and offsets.get_device() == dev
                 and (bias is None or (bias.dtype is torch.float32 and bias.shape == (E, N) and bias.is_contiguous()
                                       and bias.get_device() == dev))):
-            ldb = _i8_ld(B, 1, N, K, 16)
-            return (A.data_ptr(), _i8_ld(A, 0, T, K, 16), sA.data_ptr(), B.data_ptr(), ldb,
-                    B.stride(0) if E > 1 and K > 0 else N * ldb, sB.data_ptr(), offsets.data_ptr(), E, T, N, K,
-                    None if bias is None else bias.data_ptr(), _DTYPE16[D.dtype], D.data_ptr(),
-                    _i8_ld(D, 0, T, N, 8), kernel, _i8_stream(stream, dev))
+            if T <= 1 or N <= 1 or K == 0:
+                pad = (K + 15) // 16 * 16
+                lda, ldb = (pad if T <= 1 or K == 0 else lda), (pad if N <= 1 or K == 0 else ldb)
+                ldd = (N + 7) // 8 * 8 if T <= 1 or N == 0 else ldd
+            if E <= 1 or K == 0:
+                stride_b = N * ldb
+            return (A.data_ptr(), lda, sA.data_ptr(), B.data_ptr(), ldb, stride_b, sB.data_ptr(), offsets.data_ptr(),
+                    E, T, N, K, None if bias is None else bias.data_ptr(), _DTYPE16[D.dtype], D.data_ptr(), ldd, kernel,
+                    torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     a, b = A.shape, B.shape
     _i8_refuse([("A", A, (torch.int8,), a if len(a) == 2 else None),
                 ("B", B, (torch.int8,), (b[0], b[1], a[-1]) if len(b) == 3 else None),
-                ("D", D, tuple(_DTYPE16), (a[0], b[1]))],
+                ("D", D, tuple(_DTYPE16), (a[0], b[1] if len(b) > 1 else 0))],
                [("sA", sA, torch.float32, a[:1]), ("sB", sB, torch.float32, b[:2]),
                 ("offsets", offsets, torch.int32, (b[0] + 1,)), ("bias", bias, torch.float32, b[:2])])
 

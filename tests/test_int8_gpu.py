@@ -458,3 +458,59 @@ def test_binding_refusals():
             call()
             pytest.fail("call %d was accepted" % i)
     assert (d == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# Drawn sizes: every kernel, tile width and split that the choice reaches
+# ---------------------------------------------------------------------------
+def drawn(seed, lo, hi):
+    return int(round(np.exp(np.random.default_rng(seed).uniform(np.log(lo), np.log(hi)))))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_dense_drawn(seed):
+    M, N, K = drawn(3 * seed, 1, 1500), drawn(3 * seed + 1, 1, 3000), drawn(3 * seed + 2, 1, 3000)
+    a, sa, b, sb, bias = operands(M, N, K, seed, bias=seed % 2 == 0)
+    dtype = (BF, HF)[seed % 3 == 0]
+    got = [fp4.gemm_int8(a, sa, b, sb, bias, out_dtype=dtype, kernel=k) for k in KERNELS]
+    check_product(got[0], a, sa, b, sb, bias, (M, N, K))
+    assert all(torch.equal(g, got[0]) for g in got)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_grouped_drawn(seed):
+    rng = np.random.default_rng(1000 + seed)
+    E, rows, skew = int(rng.choice([1, 2, 5, 8, 31, 32, 33, 64, 100])), drawn(seed, 1, 2500), rng.choice([0.0, 1.0, 3.0])
+    N, K = drawn(500 + seed, 1, 900 if E > 8 else 2500), drawn(700 + seed, 1, 900)
+    p = np.exp(skew * rng.standard_normal(E))
+    counts = np.bincount(rng.choice(E, rows, p=p / p.sum()), minlength=E)
+    first, tail = int(rng.integers(0, 3)), int(rng.choice([0, 0, 7, 300]))
+    for kernel in KERNELS:
+        check_grouped(ends(*counts.tolist(), first=first), first + rows + tail, N, K, (BF, HF)[seed % 2], kernel,
+                      bias=seed % 3 == 0, seed=seed)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_grouped_captured_once_serves_any_routing(kernel):
+    # the tile lists are formed when the graph runs: from no rows to all of them in one expert
+    T, E, N, K = 700, 9, 300, 200
+    a, sa, b, sb, _ = operands(T, N, K, 21, False, experts=E)
+    b, sb = b.unflatten(0, (E, N)), sb.view(E, N)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    d = torch.zeros(T, 304, dtype=BF, device="cuda")[:, :N]
+    fp4.fp4_gemm_int8_grouped(a, sa, b, sb, off, d, kernel=kernel)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fp4.fp4_gemm_int8_grouped(a, sa, b, sb, off, d, kernel=kernel)
+    for o in ([0] * 10, [0] + [700] * 9, [0] * 9 + [700], ends(100, 0, 1, 255, 33, 0, 3, 200, 108), ends(*([1] * 9))):
+        off.copy_(torch.tensor(o, dtype=torch.int32))
+        d.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for e in range(E):
+            if o[e] < o[e + 1]:
+                s = slice(o[e], o[e + 1])
+                check_product(d[s], a[s], sa[s], b[e], sb[e], None, (o, e))
+                d[s] = 5.0
+        assert (d == 5.0).all()
