@@ -9,6 +9,10 @@ p = |sum sA sB|, y = sum sA sB + bias and u the half step of the output type
   the output's rounding adds u (|y| + that), or half of fp16's smallest
   subnormal step, 2^-25.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -99,7 +103,7 @@ def test_quantize_extreme_rows():
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("cols", [40, 3001])
+@pytest.mark.parametrize("cols", [40, 256, 3001, 4096])
 def test_quantize_zero_and_non_finite_rows(dtype, cols):
     x = torch.randn(6, cols, generator=torch.Generator().manual_seed(1)).to(dtype)
     x[1] = 0
@@ -121,7 +125,7 @@ def test_quantize_zero_and_non_finite_rows(dtype, cols):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("cols", [64, 1001, 5000])
+@pytest.mark.parametrize("cols", [64, 256, 1001, 4096, 5000])
 def test_quantize_gathers_rows(dtype, cols):
     x = torch.randn(10, (cols + 7) // 8 * 8, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()[:, :cols]
     index = torch.tensor([3, 3, 9, 0, 3, 5, 0, 9, 1, 2, 4, 6, 7, 8, 3, 3, 3], dtype=torch.int32, device="cuda")
@@ -458,6 +462,80 @@ def test_binding_refusals():
             call()
             pytest.fail("call %d was accepted" % i)
     assert (d == 0).all()
+
+
+def test_offsets_past_32_bits():
+    # three rows (or experts) that lie more than 2^31 elements apart
+    far = 2 ** 31 + 64
+    g = torch.Generator().manual_seed(17)
+    x = torch.empty(3, far, dtype=BF, device="cuda")[:, :520]
+    x.copy_(torch.randn(3, 520, generator=g).to(BF))
+    store = torch.empty(3, far, dtype=torch.int8, device="cuda")
+    codes, scales = store[:, :520], torch.empty(3, device="cuda")
+    fp4.fp4_quantize_int8(x, codes, scales)
+    check_quantized(x, codes, scales)
+    gathered, gs = fp4.quantize_int8(x, torch.tensor([2, 0, 2, 1], dtype=torch.int32, device="cuda"))
+    check_quantized(x[[2, 0, 2, 1]], gathered, gs)
+    del x
+    b, sb = random_codes(g, 40, 520), torch.rand(40, generator=g).cuda()
+    d = torch.empty(3, far, dtype=BF, device="cuda")[:, :40]
+    for kernel in KERNELS:
+        d.zero_()
+        fp4.fp4_gemm_int8(codes, scales, b, sb, d, kernel=kernel)                  # far rows of A and D
+        check_product(d, codes, scales, b, sb, None)
+        y = fp4.gemm_int8(b, sb, codes, scales, kernel=kernel)                     # far rows of B
+        check_product(y, b, sb, codes, scales, None)
+    experts = store.as_strided((3, 5, 96), (far, 96, 1))
+    experts.copy_(torch.randint(-128, 128, (3, 5, 96), generator=g, dtype=torch.int8))
+    a, sa, se = random_codes(g, 9, 96), torch.rand(9, generator=g).cuda(), torch.rand(3, 5, generator=g).cuda()
+    off = torch.tensor([0, 2, 5, 9], dtype=torch.int32, device="cuda")
+    for kernel in KERNELS:
+        y = fp4.gemm_int8_grouped(a, sa, experts, se, off, kernel=kernel)
+        for e, (lo, hi) in enumerate(((0, 2), (2, 5), (5, 9))):
+            check_product(y[lo:hi], a[lo:hi], sa[lo:hi], experts[e], se[e], None)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_expert_stride_is_no_multiple_of_the_rows(kernel):
+    g = torch.Generator().manual_seed(18)
+    store = torch.randint(-128, 128, (4000,), generator=g, dtype=torch.int8).cuda()
+    b = store[16:].as_strided((4, 11, 20), (11 * 48 + 16, 48, 1), store.storage_offset() + 16)
+    a, sa, sb = random_codes(g, 14, 20), torch.rand(14, generator=g).cuda(), torch.rand(4, 11, generator=g).cuda()
+    y = fp4.gemm_int8_grouped(a, sa, b, sb, torch.tensor([0, 3, 7, 8, 14], dtype=torch.int32, device="cuda"), kernel=kernel)
+    for e, (lo, hi) in enumerate(((0, 3), (3, 7), (7, 8), (8, 14))):
+        check_product(y[lo:hi], a[lo:hi], sa[lo:hi], b[e], sb[e], None)
+
+
+FIRST_CALL = """
+import sys
+sys.path.insert(0, %r)
+import torch
+from block_scaled_fp4_05_b200 import fp4
+x = torch.randn(%d, 256, device="cuda").bfloat16()
+w = torch.randint(-127, 128, (300, 256), dtype=torch.int8, device="cuda")
+sw = torch.rand(300, device="cuda")
+off = torch.tensor([0, %d], dtype=torch.int32, device="cuda")
+d, e = (torch.zeros(%d, 304, dtype=torch.bfloat16, device="cuda")[:, :300] for _ in range(2))
+codes, scales = torch.empty(%d, 256, dtype=torch.int8, device="cuda"), torch.empty(%d, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    fp4.fp4_quantize_int8(x, codes, scales)
+    fp4.fp4_gemm_int8(codes, scales, w, sw, d)
+    fp4.fp4_gemm_int8_grouped(codes, scales, w[None], sw[None], off, e)
+graph.replay()
+torch.cuda.synchronize()
+y = (codes.double() @ w.double().T * scales.double()[:, None] * sw.double()).float()
+assert torch.equal(d, e) and ((d.float() - y).abs() <= (2.0 ** -8 + 2.0 ** -20) * y.abs() + 1e-6).all()
+assert fp4.fp4_get_device_status() == 0
+"""
+
+
+@pytest.mark.parametrize("M", [9, 600])
+def test_first_calls_of_a_process_are_captured(M):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL % (root, M, M, M, M, M)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------------------
