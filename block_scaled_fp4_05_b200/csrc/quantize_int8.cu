@@ -8,15 +8,13 @@
 // integers times powers of two, so 127 x_k / amax is either exactly halfway
 // between two integers or at least 2^-19 (relative) away from it; an FP32
 // quotient within an ulp rounds to the same integer unless it is a tie, and a
-// tie has to come out exact.  With the row scaled by a power of two (exact,
-// so that neither 127 x nor 1 / amax leaves the FP32 range) and r the
-// approximate reciprocal of amax (within 2^-22 of it):
-//   t = RN(a r), a = 127 x;  e = a - t amax (exact as an FMA: it cancels to a
-//   few bits);  q = RN(t + e r)
-// t + e r differs from the quotient by less than 2^-42 of it, so a quotient
-// that FP32 holds (every tie does) comes out exactly.  Adding 1.5 * 2^23 rounds
-// q to an integer, halves to even, and leaves its two's complement in the low
-// byte.  Two elements go through these steps in one instruction each.
+// tie has to come out exactly.  So 127 / amax is held as the sum of two floats
+// h + l, within 2^-44 of it (h the product with the approximate reciprocal, l
+// from the residual 127 - h amax, which an FMA gives exactly), and
+//   t = RN(x h + RN(x l))
+// is a quotient that FP32 holds (every tie is one) exactly.  Adding 1.5 * 2^23
+// rounds t to an integer, halves to even, and leaves its two's complement in
+// the low byte.  Three instructions for two elements.
 //
 // Bound by HBM: 2 bytes read and 1 written an element.  A row stays in the
 // registers of its threads between the maximum and the codes, so it is read
@@ -25,8 +23,8 @@
 // keep more loads in flight than blocks that load a row ahead while they work
 // on one (8194 rows of 4096: 18.9, two rows a block 19.5, eight 21.7 us).
 // Measured on a B200, of 6559 GB/s: 8192x8192 31.1 us (99 %), 8194x4096 16.3
-// us (94 %); 8194 rows gathered from 4097 of 4096 17.2 us, where instructions
-// bind (about ten an element, 70 % of the issue slots).
+// us (94 %); 8194 rows gathered from 4097 of 4096 16.6 us, where latency and
+// instructions bind (59 % of the issue slots), not HBM.
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -39,11 +37,10 @@
 namespace fp4 {
 namespace {
 
-// One row's multipliers: a = 127 x is x * c, the scaled maximum is m.
+// One row's multipliers: 127 / (amax * pre) = hi + lo, for elements times pre.
 struct RowScale {
-    float c;      // 127 * 2^p
-    float m;      // amax * 2^p
-    float r;      // about 1 / m
+    float hi, lo;
+    float pre;   // a power of two; 1 unless amax is so small or so large that hi or lo left the FP32 range
 };
 
 template <bool HALF>
@@ -57,14 +54,20 @@ template <bool HALF>
 __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits)
 {
     RowScale s;
-    const float amax = widen<HALF>(amax_bits);
-    // 2^p brings a normal maximum into [4, 8); p is capped at 120, so that
-    // 127 * 2^p is finite (subnormal BF16 maxima then end below 4)
-    const int eb = (int)(__float_as_uint(amax) >> 23);
-    const float p = __uint_as_float((uint32_t)min(256 - eb, 247) << 23);
-    s.c = 127.0f * p;
-    s.m = amax_bits ? amax * p : 1.0f;   // a row of zeros: any
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.r) : "f"(s.m));
+    float m = amax_bits ? widen<HALF>(amax_bits) : 1.0f;   // a row of zeros: any
+    s.pre = 1.0f;
+    if (!HALF) {
+        const int eb = (int)(__float_as_uint(m) >> 23);
+        if (eb < 27 || eb > 242) {   // outside [2^-100, 2^116)
+            // into [4, 8); a subnormal maximum ends below
+            s.pre = __uint_as_float((uint32_t)min(256 - eb, 247) << 23);
+            m *= s.pre;
+        }
+    }
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m));
+    s.hi = __fmul_rn(127.0f, r);
+    s.lo = __fmul_rn(__fmaf_rn(-s.hi, m, 127.0f), r);
     return s;
 }
 
@@ -104,20 +107,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
-// The codes of two elements in the low bytes of the halves (other bytes: garbage).
-__device__ __forceinline__ uint64_t code2(uint64_t x, uint64_t c, uint64_t neg_m, uint64_t r)
-{
-    const uint64_t a = mul2(x, c);
-    const uint64_t t = mul2(a, r);
-    const uint64_t q = fma2(fma2(t, neg_m, a), r, t);
-    return add2(q, pair(12582912.0f, 12582912.0f));
-}
-
 template <bool HALF>
 __device__ __forceinline__ uint2 codes8(uint4 v, const RowScale& s, bool finite)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    const uint64_t c = pair(s.c, s.c), neg_m = pair(-s.m, -s.m), r = pair(s.r, s.r);
+    const uint64_t hi2 = pair(s.hi, s.hi), lo2 = pair(s.lo, s.lo), round2 = pair(12582912.0f, 12582912.0f);
     uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -130,7 +124,9 @@ __device__ __forceinline__ uint2 codes8(uint4 v, const RowScale& s, bool finite)
             lo = __uint_as_float(w[i] << 16);
             hi = __uint_as_float(w[i] & 0xFFFF0000u);
         }
-        const uint64_t q = code2(pair(lo, hi), c, neg_m, r);
+        uint64_t x = pair(lo, hi);
+        if (!HALF && s.pre != 1.0f) x = mul2(x, pair(s.pre, s.pre));   // (a row's choice)
+        const uint64_t q = add2(fma2(x, hi2, mul2(x, lo2)), round2);
         b[i] = __byte_perm((uint32_t)q, (uint32_t)(q >> 32), 0x0040);
     }
     if (!finite) return make_uint2(0u, 0u);
