@@ -7,17 +7,24 @@ division, reciprocal and products) and links the CUDA runtime dynamically.
 The driver API (tensor-map encoding) is reached at run time through the
 runtime's entry-point query, so libcuda is not a link dependency and the
 library loads on machines without a GPU.
+
+The Python calls of the INT8 entry points (csrc/int8_calls.cpp) are a small
+extension module beside it, _int8_calls.so, compiled by g++ against torch's
+headers: host code alone, which takes its entry points from libfp4.so.
 """
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp4.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "quantize_int8.cu", "gemm_int8.cu"]
 HEADERS = ["fp4_internal.h", "quant_device.cuh", "tc_device.cuh"]
+CALLS = os.path.join(HERE, "_int8_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "int8_calls.cpp")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC_FLAGS = [
@@ -45,11 +52,36 @@ def _inputs():
     return files
 
 
+def _newer(out, inputs):
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in inputs)
+
+
 def up_to_date():
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return (_newer(LIB, _inputs())
+            and _newer(CALLS, [CALLS_SOURCE, os.path.join(INCLUDE, "fp4.h")]))
+
+
+def build_calls(verbose=False):
+    """_int8_calls.so: torch (already loaded wherever it is imported) provides
+    every symbol that it does not define."""
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wno-attributes",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(home, "include"),
+           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+           "-I", sysconfig.get_paths()["include"], "-o", tmp, CALLS_SOURCE,
+           "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + r.stdout + r.stderr)
+    if verbose:
+        sys.stderr.write(r.stdout + r.stderr)
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(force=False, verbose=False):
@@ -66,6 +98,7 @@ def build(force=False, verbose=False):
     if verbose:
         sys.stderr.write(r.stdout + r.stderr)
     os.replace(tmp, LIB)
+    build_calls(verbose)
     return LIB
 
 

@@ -335,13 +335,28 @@ def bind_gemm_decode_dynamic(x, W, sW, gsW, D, gs_out, alpha_out, workspace, str
 # INT8 layers: one scale per token (row of A) and per output channel (row of B)
 # ---------------------------------------------------------------------------
 _DTYPE16 = {torch.bfloat16: BF16, torch.float16: FP16}
+_calls = None
 
 
-# The leading dimension of a single row, or of rows without elements, is never
-# used: the functions below count it as the next multiple of 16 (8 for 16-bit
-# types) bytes.  They check a call that fits in one expression, with as few
-# tensor accesses as that takes (a call's Python part is 3 to 4 us), and leave
-# it to _i8_refuse to find what does not fit.
+def _int8_calls():
+    """The extension module that checks and marshals these calls (raises if it
+    has not been built)."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _int8_calls as m
+        except ImportError as e:
+            raise RuntimeError("_int8_calls.so is missing; build it with "
+                               "`python -m block_scaled_fp4_05_b200.build`") from e
+        m.set_entry_points(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                             (L.fp4_quantize_int8, L.fp4_gemm_int8, L.fp4_gemm_int8_grouped)))
+        _calls = m
+    return _calls
+
+
+def _i8_stream(stream):
+    return None if stream is None else _stream(stream).value or 0
 
 
 def _i8_refuse(matrices, vectors):
@@ -365,133 +380,82 @@ def _i8_refuse(matrices, vectors):
     raise ValueError("the tensors do not fit together")
 
 
-def _quantize_int8_args(x, codes, scales, row_index, stream):
-    dev = torch.cuda.current_device()
-    if x.dim() == 2 and codes.dim() == 2:
-        (rows_in, cols), (rows, ccols) = x.shape, codes.shape
-        (ld, unit), (ldc, cunit) = x.stride(), codes.stride()
-        if (cols == ccols and x.dtype in _DTYPE16 and codes.dtype is torch.int8
-                and scales.dtype is torch.float32 and scales.shape == (rows,) and scales.is_contiguous()
-                and (unit == cunit == 1 or cols <= 1)
-                and x.get_device() == dev and codes.get_device() == dev and scales.get_device() == dev
-                and (rows_in == rows if row_index is None else
-                     row_index.dtype is torch.int32 and row_index.shape == (rows,) and row_index.is_contiguous()
-                     and row_index.get_device() == dev)):
-            if rows_in <= 1 or cols == 0:
-                ld = (cols + 7) // 8 * 8
-            if rows <= 1 or cols == 0:
-                ldc = (cols + 15) // 16 * 16
-            return (x.data_ptr(), _DTYPE16[x.dtype], rows_in, cols, ld,
-                    None if row_index is None else row_index.data_ptr(), rows, codes.data_ptr(), ldc,
-                    scales.data_ptr(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+def _refuse_quantize(x, codes, scales, row_index, stream=None):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x has to be a matrix")
     rows = len(x) if row_index is None else len(row_index)
-    _i8_refuse([("x", x, tuple(_DTYPE16), x.shape if x.dim() == 2 else None),
-                ("codes", codes, (torch.int8,), (rows,) + tuple(x.shape[1:]))],
+    _i8_refuse([("x", x, tuple(_DTYPE16), x.shape), ("codes", codes, (torch.int8,), (rows, x.shape[1]))],
                [("scales", scales, torch.float32, (rows,)), ("row_index", row_index, torch.int32, (rows,))])
+
+
+def _refuse_gemm(A, sA, B, sB, D, bias, kernel, stream=None, offsets=None, experts=False):
+    dims = 3 if experts else 2
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise TypeError("A has to be a matrix")
+    if not isinstance(B, torch.Tensor) or B.dim() != dims:
+        raise TypeError("B has to be a tensor of %d dimensions" % dims)
+    (M, K), channels = A.shape, B.shape[:-1]
+    _i8_refuse([("A", A, (torch.int8,), (M, K)), ("B", B, (torch.int8,), tuple(channels) + (K,)),
+                ("D", D, tuple(_DTYPE16), (M, channels[-1]))],
+               [("sA", sA, torch.float32, (M,)), ("sB", sB, torch.float32, channels), ("bias", bias, torch.float32, channels)]
+               + ([("offsets", offsets, torch.int32, (channels[0] + 1,))] if experts else []))
 
 
 def fp4_quantize_int8(x, codes, scales, row_index=None, stream=None):
     """Per-row INT8 quantization of x [R x C] (bf16 or fp16) into codes (int8)
     and scales (float32): scales = amax / 127, codes = 127 x / amax rounded to
     nearest even.  With row_index (int32) output row r is x[row_index[r]]."""
-    st = lib().fp4_quantize_int8(*_quantize_int8_args(x, codes, scales, row_index, stream))
+    st = (_calls or _int8_calls()).quantize(x, codes, scales, row_index, _i8_stream(stream))
     if st != FP4_OK:
+        if st < 0:
+            _refuse_quantize(x, codes, scales, row_index)
         _check(st, "fp4_quantize_int8")
 
 
 def bind_quantize_int8(x, codes, scales, row_index=None, stream=None):
-    call = BoundCall("fp4_quantize_int8", *_quantize_int8_args(x, codes, scales, row_index, stream))
+    args = _int8_calls().quantize_args(x, codes, scales, row_index, _i8_stream(stream))
+    if args is None:
+        _refuse_quantize(x, codes, scales, row_index)
+    call = BoundCall("fp4_quantize_int8", *args)
     call.keep = (x, codes, scales, row_index)
     return call
-
-
-def _gemm_int8_args(A, sA, B, sB, D, bias, kernel, stream):
-    dev = torch.cuda.current_device()
-    if A.dim() == 2 and B.dim() == 2 and D.dim() == 2:
-        (M, K), (N, KB) = A.shape, B.shape
-        (lda, ua), (ldb, ub), (ldd, ud) = A.stride(), B.stride(), D.stride()
-        if (KB == K and D.shape == (M, N)
-                and A.dtype is torch.int8 and B.dtype is torch.int8 and D.dtype in _DTYPE16
-                and sA.dtype is torch.float32 and sA.shape == (M,) and sA.is_contiguous()
-                and sB.dtype is torch.float32 and sB.shape == (N,) and sB.is_contiguous()
-                and (ua == ub == 1 or K <= 1) and (ud == 1 or N <= 1)
-                and A.get_device() == dev and B.get_device() == dev and D.get_device() == dev
-                and sA.get_device() == dev and sB.get_device() == dev
-                and (bias is None or (bias.dtype is torch.float32 and bias.shape == (N,) and bias.is_contiguous()
-                                      and bias.get_device() == dev))):
-            if M <= 1 or N <= 1 or K == 0:
-                pad = (K + 15) // 16 * 16
-                lda, ldb = (pad if M <= 1 or K == 0 else lda), (pad if N <= 1 or K == 0 else ldb)
-                ldd = (N + 7) // 8 * 8 if M <= 1 or N == 0 else ldd
-            return (A.data_ptr(), lda, sA.data_ptr(), B.data_ptr(), ldb, sB.data_ptr(), M, N, K,
-                    None if bias is None else bias.data_ptr(), _DTYPE16[D.dtype], D.data_ptr(), ldd, kernel,
-                    torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    a, b = A.shape, B.shape
-    _i8_refuse([("A", A, (torch.int8,), a if len(a) == 2 else None),
-                ("B", B, (torch.int8,), (b[0], a[-1]) if len(b) == 2 else None),
-                ("D", D, tuple(_DTYPE16), (a[0], b[0]))],
-               [("sA", sA, torch.float32, a[:1]), ("sB", sB, torch.float32, b[:1]),
-                ("bias", bias, torch.float32, b[:1])])
 
 
 def fp4_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
     """D [M x N] (bf16 or fp16) = (A @ B^T) * sA[:, None] * sB + bias for int8
     A [M x K] and B [N x K]: exact integer sums, scaled and rounded once."""
-    st = lib().fp4_gemm_int8(*_gemm_int8_args(A, sA, B, sB, D, bias, kernel, stream))
+    st = (_calls or _int8_calls()).gemm(A, sA, B, sB, D, bias, kernel, _i8_stream(stream))
     if st != FP4_OK:
+        if st < 0:
+            _refuse_gemm(A, sA, B, sB, D, bias, kernel)
         _check(st, "fp4_gemm_int8")
 
 
 def bind_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
-    call = BoundCall("fp4_gemm_int8", *_gemm_int8_args(A, sA, B, sB, D, bias, kernel, stream))
+    args = _int8_calls().gemm_args(A, sA, B, sB, D, bias, kernel, _i8_stream(stream))
+    if args is None:
+        _refuse_gemm(A, sA, B, sB, D, bias, kernel)
+    call = BoundCall("fp4_gemm_int8", *args)
     call.keep = (A, sA, B, sB, D, bias)
     return call
-
-
-def _gemm_int8_grouped_args(A, sA, B, sB, offsets, D, bias, kernel, stream):
-    dev = torch.cuda.current_device()
-    if A.dim() == 2 and B.dim() == 3 and D.dim() == 2:
-        (T, K), (E, N, KB) = A.shape, B.shape
-        (lda, ua), (stride_b, ldb, ub), (ldd, ud) = A.stride(), B.stride(), D.stride()
-        if (KB == K and D.shape == (T, N)
-                and A.dtype is torch.int8 and B.dtype is torch.int8 and D.dtype in _DTYPE16
-                and sA.dtype is torch.float32 and sA.shape == (T,) and sA.is_contiguous()
-                and sB.dtype is torch.float32 and sB.shape == (E, N) and sB.is_contiguous()
-                and offsets.dtype is torch.int32 and offsets.shape == (E + 1,) and offsets.is_contiguous()
-                and (ua == ub == 1 or K <= 1) and (ud == 1 or N <= 1)
-                and A.get_device() == dev and B.get_device() == dev and D.get_device() == dev
-                and sA.get_device() == dev and sB.get_device() == dev and offsets.get_device() == dev
-                and (bias is None or (bias.dtype is torch.float32 and bias.shape == (E, N) and bias.is_contiguous()
-                                      and bias.get_device() == dev))):
-            if T <= 1 or N <= 1 or K == 0:
-                pad = (K + 15) // 16 * 16
-                lda, ldb = (pad if T <= 1 or K == 0 else lda), (pad if N <= 1 or K == 0 else ldb)
-                ldd = (N + 7) // 8 * 8 if T <= 1 or N == 0 else ldd
-            if E <= 1 or K == 0:
-                stride_b = N * ldb
-            return (A.data_ptr(), lda, sA.data_ptr(), B.data_ptr(), ldb, stride_b, sB.data_ptr(), offsets.data_ptr(),
-                    E, T, N, K, None if bias is None else bias.data_ptr(), _DTYPE16[D.dtype], D.data_ptr(), ldd, kernel,
-                    torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    a, b = A.shape, B.shape
-    _i8_refuse([("A", A, (torch.int8,), a if len(a) == 2 else None),
-                ("B", B, (torch.int8,), (b[0], b[1], a[-1]) if len(b) == 3 else None),
-                ("D", D, tuple(_DTYPE16), (a[0], b[1] if len(b) > 1 else 0))],
-               [("sA", sA, torch.float32, a[:1]), ("sB", sB, torch.float32, b[:2]),
-                ("offsets", offsets, torch.int32, (b[0] + 1,)), ("bias", bias, torch.float32, b[:2])])
 
 
 def fp4_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias=None, kernel=GEMM_AUTO, stream=None):
     """fp4_gemm_int8 by expert: rows offsets[e] .. offsets[e + 1] of A and D
     with B[e] [N x K], sB[e] and bias[e].  offsets (int32, E + 1) is read on
     the device; rows of D in no group are left as they were."""
-    st = lib().fp4_gemm_int8_grouped(*_gemm_int8_grouped_args(A, sA, B, sB, offsets, D, bias, kernel, stream))
+    st = (_calls or _int8_calls()).grouped(A, sA, B, sB, offsets, D, bias, kernel, _i8_stream(stream))
     if st != FP4_OK:
+        if st < 0:
+            _refuse_gemm(A, sA, B, sB, D, bias, kernel, offsets=offsets, experts=True)
         _check(st, "fp4_gemm_int8_grouped")
 
 
 def bind_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias=None, kernel=GEMM_AUTO, stream=None):
-    call = BoundCall("fp4_gemm_int8_grouped",
-                     *_gemm_int8_grouped_args(A, sA, B, sB, offsets, D, bias, kernel, stream))
+    args = _int8_calls().grouped_args(A, sA, B, sB, offsets, D, bias, kernel, _i8_stream(stream))
+    if args is None:
+        _refuse_gemm(A, sA, B, sB, D, bias, kernel, offsets=offsets, experts=True)
+    call = BoundCall("fp4_gemm_int8_grouped", *args)
     call.keep = (A, sA, B, sB, offsets, D, bias)
     return call
 
