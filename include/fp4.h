@@ -108,7 +108,8 @@ typedef enum {
     FP4_FP16 = 1
 } fp4_dtype;
 
-/* Version of this ABI (incremented on any signature or contract change). */
+/* Version of this ABI (incremented on any change of a signature or contract;
+ * additions leave it). */
 int fp4_abi_version(void);
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -453,10 +454,14 @@ fp4_status fp4_quantize_int8(const void* in, fp4_dtype in_dtype, int64_t rows_in
  *   bias : device, N floats, or NULL for none
  *   D : device, [M x N] of out_dtype, leading dimension ldd; the elements
  *       between N and ldd are not written
- *   kernel : FP4_GEMM_AUTO; FP4_GEMM_PREFILL: CTA pairs, 256 x 256 or
- *       256 x 128 tiles; FP4_GEMM_DECODE: weights on the 128-row side, K
- *       split over a cluster.  Either takes any M; they give the same bits.
- *       FP4_GEMM_B_STATIC may be OR-ed as for fp4_gemm (here for B alone).
+ *   kernel : FP4_GEMM_PREFILL: CTA pairs, tiles of 256 channels x 32 to 256
+ *       tokens; FP4_GEMM_DECODE: tiles of 128 channels x 16 to 128 tokens, K
+ *       split over a cluster where the tiles are few; FP4_GEMM_AUTO: the one
+ *       that takes less time by an estimate from the sizes.  Either takes any
+ *       M, and both give the same bits.  FP4_GEMM_B_STATIC may be OR-ed: B is
+ *       not written by a kernel that may still be running on the stream when
+ *       this one starts, so its first tiles are requested before that kernel
+ *       has ended.
  * M, N and K may be any numbers (M == 0 or N == 0: a no-op; K == 0: the sums
  * are 0) up to K <= 131071, above which a sum of products of -128 could leave
  * 32 bits.  Requires lda, ldb % 16 == 0, ldd % 8 == 0, 16-byte aligned A, B
@@ -479,7 +484,7 @@ fp4_status fp4_gemm_int8(const void* A, int64_t lda, const float* sA, const void
  *             and raised to the largest one before them.
  *   E : 0 <= E <= 512;  T : rows of A, sA and D
  * Rows of D before offsets[0] and from offsets[E] on are left as they were;
- * experts without rows cost nothing.  FP4_GEMM_AUTO chooses by T / E.
+ * experts without rows cost nothing.  FP4_GEMM_AUTO estimates from T / E.
  * Requires stride_b % 16 == 0 and stride_b >= (N - 1) * ldb + K, else as
  * fp4_gemm_int8.
  */
