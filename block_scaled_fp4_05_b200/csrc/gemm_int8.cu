@@ -43,6 +43,8 @@ constexpr int I8_BK = 128;          // K elements (and bytes a row) per stage
 constexpr int I8_MMA_K = 32;        // K per tcgen05.mma kind::i8
 constexpr int I8_TILE = I8_BM * I8_BK;
 constexpr int kMaxExperts = kInt8MaxExperts;
+constexpr int kMaxSmem = 232448;    // dynamic shared memory of a block
+constexpr int kSmSmem = 233472;     // of an SM; each block there takes 1 KB more than it asks for
 constexpr int64_t kI8GroupBytes = int64_t(32) << 20;
 
 struct I8Params {
@@ -54,9 +56,9 @@ struct I8Params {
     int32_t M, N;            // rows of A and D, output channels
     int32_t ks_total;        // stages of a tile (0: K = 0, the sums are zero)
     int32_t tiles_n;         // channel tiles
-    // pair kernel: most tokens of a tile and the stages that fit, token tiles
-    // per group of the tile order
-    int32_t bt, stages, raster_gm;
+    int32_t stages;          // of the ring
+    // pair kernel: most tokens of a tile, token tiles per group of the tile order
+    int32_t bt, raster_gm;
     int32_t E;               // experts (dense: 1)
     const int32_t* offsets;  // [E + 1] (dense: NULL, one group of all M rows)
     int32_t b_static;        // B is not written by the previous kernel
@@ -196,21 +198,20 @@ __device__ __forceinline__ void expert_bounds(const I8Params& p, int e0, int lan
 // result), each CTA for 128 / S channels, scale, and store 8 bytes at a time.
 // ------------------------------------------------------------------------
 constexpr int kSwapThreads = 256;
-constexpr int swap_resident(int nt) { return nt == 16 ? 3 : 2; }   // CTAs an SM holds
+constexpr int swap_resident(int nt) { return nt == 16 ? 3 : 2; }   // CTAs an SM holds, at most
 
 template <int NT>
 struct SwapCfg {
-    // Two to three CTAs share an SM, so that one's first loads and last
-    // stores overlap another's stream: 72 to 100 KB each.
-    static constexpr int STAGES = NT == 16 ? 4 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+    static constexpr int MAX_STAGES = 12;
     static constexpr int STAGE_BYTES = I8_TILE + NT * I8_BK;
     static constexpr int OFF_T = I8_TILE;
-    static constexpr int OFF_BARS = STAGES * STAGE_BYTES;
-    static constexpr int OFF_SCALE = OFF_BARS + 256;   // sA of the tokens, sB and bias of the channels
-    static constexpr int SMEM = OFF_SCALE + (NT + 2 * I8_BM) * 4 + 1024;
+    // before the stages: barriers, sA of the tokens, sB and bias of the channels
+    static constexpr int OFF_SCALE = 256;
+    static constexpr int FIXED = (OFF_SCALE + (NT + 2 * I8_BM) * 4 + 1023) / 1024 * 1024;
+    static constexpr int MIN_STAGES = (NT * I8_BM * 4 + STAGE_BYTES - 1) / STAGE_BYTES;   // the sums reuse their memory
     static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
-    static_assert(NT * I8_BM * 4 <= OFF_BARS, "the sums reuse the stages' memory");
-    static_assert((2 * STAGES + 1) * 8 + 40 <= 256, "barrier area");
+    static constexpr int smem(int stages) { return 1024 + FIXED + stages * STAGE_BYTES; }
+    static_assert((2 * MAX_STAGES + 1) * 8 + 40 <= OFF_SCALE, "barrier area");
 };
 
 // Adds the S CTAs' sums for this CTA's channels, scales and stores.  A thread
@@ -274,13 +275,13 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                  const I8Params p)
 {
     using C = SwapCfg<NT>;
-    constexpr int STAGES = C::STAGES;
+    const int stages = p.stages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
-    // [0,S) full, [S,2S) empty, [2S] accumulator full
-    int* shared_word = reinterpret_cast<int*>(bars + 2 * STAGES + 1);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+    // [0,12) full, [12,24) empty, [24] accumulator full
+    int* shared_word = reinterpret_cast<int*>(bars + 2 * C::MAX_STAGES + 1);
     // [0] tensor-memory base, [1] abort; [2..5] and [6..9] the item (grouped,
     // even and odd ones): expert (-1: none), first row, rows, tile within the expert
     volatile int* abort_flag = shared_word + 1;
@@ -294,11 +295,11 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int rank = (int)cluster_rank();
     const int kb = (int)((int64_t)p.ks_total * rank / (int)split);
     const int ke = (int)((int64_t)p.ks_total * (rank + 1) / (int)split);
-    const uint32_t smem0 = smem_u32(smem);
+    const uint32_t smem0 = smem_u32(smem) + C::FIXED;   // first stage
     const uint32_t bar0 = smem_u32(bars);
     auto FULL = [&](int s) { return bar0 + 8u * s; };
-    auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    const uint32_t acc_full = bar0 + 8u * (2 * STAGES);
+    auto EMPTY = [&](int s) { return bar0 + 8u * (C::MAX_STAGES + s); };
+    const uint32_t acc_full = bar0 + 8u * (2 * C::MAX_STAGES);
     // Items: the tiles (expert, channel tile, token tile), token tiles
     // fastest so that clusters that share weights run next to each other,
     // dealt round-robin to the clusters.
@@ -306,10 +307,10 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int dense_mt = (p.M + NT - 1) / NT;
     // Weight tiles requested before the dependency wait (static weights of a
     // dense product): those of the first stages, their token tiles follow.
-    int pre = !p.offsets && p.b_static ? min(STAGES, ke - kb) : 0;
+    int pre = !p.offsets && p.b_static ? min(stages, ke - kb) : 0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(FULL(s), 1);
             mbar_init(EMPTY(s), 1);
         }
@@ -396,7 +397,7 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                         tma_load_3d(&tmW, FULL(stage), st, ks * I8_BK, tn * I8_BM, expert);
                     }
                     tma_load_2d(&tmX, FULL(stage), st + C::OFF_T, ks * I8_BK, row0);
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -421,7 +422,7 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                         mma_i8(tmem_base, adesc0 + step + 2 * j, bdesc0 + step + 2 * j, idesc_i8(I8_BM, NT),
                                (ks > kb || j > 0) ? 1u : 0u);
                     tc_commit(EMPTY(stage));
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -528,7 +529,7 @@ struct I8Pair {
     static constexpr int OFF_BARS = OFF_LIST + 2 * (kMaxExperts + 2) * 4;
     static constexpr int NBARS = 2 * kI8PairMaxStages + 5;
     static constexpr int FIXED = (OFF_BARS + 256 + 1023) / 1024 * 1024;       // what lies before the stages
-    static constexpr int SMEM = 232448;
+    static constexpr int SMEM = kMaxSmem;
     static constexpr int STAGE_ROOM = SMEM - 1024 - FIXED;
     static_assert(NBARS * 8 + 8 <= 256, "barrier area");
     static_assert(OFF_BARS % 16 == 0, "barrier alignment");
@@ -981,6 +982,20 @@ I8Params params_of(const Int8GemmArgs& a, int bn)
     return p;
 }
 
+// Stages of the few-token kernel: those of a CTA's share of K, as far as they
+// fit beside the other CTAs of the SM.
+template <int NT>
+int swap_stages(unsigned grid, int share, int sm_count)
+{
+    using C = SwapCfg<NT>;
+    int ctas = (int)((grid + sm_count - 1) / sm_count);
+    if (ctas > swap_resident(NT)) ctas = swap_resident(NT);
+    const int room = (kSmSmem / ctas - 1024 - C::smem(0)) / C::STAGE_BYTES;
+    int n = share < room ? share : room;
+    if (n > C::MAX_STAGES) n = C::MAX_STAGES;
+    return n < C::MIN_STAGES ? C::MIN_STAGES : n;
+}
+
 template <int NT, bool HALF>
 cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, int sm_count, cudaStream_t s)
 {
@@ -993,14 +1008,17 @@ cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, int 
     }
     static uint64_t done = 0;
     auto kern = int8_swap_kernel<NT, HALF>;
-    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), C::SMEM, done);
+    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), C::smem(C::MAX_STAGES) < kMaxSmem ? C::smem(C::MAX_STAGES) : kMaxSmem, done);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         // as many clusters as the SMs hold take all tiles in turn
         const int64_t hold = (int64_t)swap_resident(NT) * sm_count / split;
-        launch_config(cfg, attr, (unsigned)((clusters < hold ? clusters : hold) * split), kSwapThreads, (unsigned)split, C::SMEM, s);
-        e = cudaLaunchKernelEx(&cfg, kern, tw, tx, params_of(a, I8_BM));
+        const unsigned grid = (unsigned)((clusters < hold ? clusters : hold) * split);
+        I8Params p = params_of(a, I8_BM);
+        p.stages = swap_stages<NT>(grid, (p.ks_total + split - 1) / split, sm_count);
+        launch_config(cfg, attr, grid, kSwapThreads, (unsigned)split, C::smem(p.stages), s);
+        e = cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
     }
     if (e != cudaSuccess) set_last_error("INT8 GEMM launch (few tokens)", e);
     return e;
