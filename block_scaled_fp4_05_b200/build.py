@@ -21,8 +21,8 @@ import sysconfig
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp4.so")
-SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "quantize_int8.cu", "gemm_int8.cu"]
-HEADERS = ["fp4_internal.h", "quant_device.cuh", "tc_device.cuh"]
+SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "quantize_int8.cu", "gemm_int8.cu", "gemv_int8.cu"]
+HEADERS = ["fp4_internal.h", "quant_device.cuh", "tc_device.cuh", "int8_device.cuh"]
 CALLS = os.path.join(HERE, "_int8_calls.so")
 CALLS_SOURCE = os.path.join(CSRC, "int8_calls.cpp")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")

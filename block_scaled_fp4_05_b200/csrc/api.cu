@@ -97,6 +97,7 @@ constexpr int64_t kMaxRowTiles = (int64_t)1 << 28;
 // INT8 products: exact 32-bit sums for any codes, tile counts in 32 bits,
 // strides a tensor map can hold.
 constexpr int64_t kInt8MaxK = 131071;
+constexpr int64_t kMaxInt8Rows = (int64_t)1 << 30;
 constexpr int64_t kMaxInt8Tiles = (int64_t)1 << 26;   // of 256 x 128; D has terabytes there
 constexpr int64_t kMaxMapStride = (int64_t)1 << 40;
 constexpr int64_t kMaxInt8Cols = (int64_t)1 << 30;   // the quantizer indexes a row in 32 bits
@@ -608,7 +609,7 @@ static fp4_status gemm_int8(const void* A, int64_t lda, const float* sA, const v
     if (!D || !sA || !sB) return FP4_ERR_INVALID_ARG;
     if (K > 0 && (!A || !B)) return FP4_ERR_INVALID_ARG;
     // K: 128 * 128 * K stays below 2^31.  M, N: tile counts in 32 bits.
-    if (K > kInt8MaxK || M >= kMaxRows || N >= kMaxRows) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (K > kInt8MaxK || M > kMaxInt8Rows || N > kMaxInt8Rows) return FP4_ERR_UNSUPPORTED_SHAPE;
     if ((M / 256 + E) * ((N + 127) / 128) > kMaxInt8Tiles) return FP4_ERR_UNSUPPORTED_SHAPE;
     // tensor-map strides are below 2^40 bytes
     if (lda >= kMaxMapStride || ldb >= kMaxMapStride || stride_b >= kMaxMapStride || ldd >= kMaxMapStride / 2)

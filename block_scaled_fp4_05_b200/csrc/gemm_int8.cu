@@ -14,6 +14,7 @@
 //                      through distributed shared memory.  Bound by HBM (the
 //                      weights are read once).
 // Both have the weights on the MMA's fixed side and the tokens on the other.
+// (gemv_int8.cu has a third, dot products, for the smallest.)
 // Scales, bias and offsets are read past L1 (they may be written by the kernel
 // before, which can still be running when these kernels start).
 // Both take a grouped launch's tile list from the offsets themselves, so a
@@ -33,10 +34,14 @@
 #include <mutex>
 
 #include "fp4_internal.h"
+#include "int8_device.cuh"
 #include "tc_device.cuh"
 
 namespace fp4 {
 namespace {
+
+using i8::pack16;
+using i8::scaled;
 
 constexpr int I8_BM = 128;          // rows of the A-side operand per CTA
 constexpr int I8_BK = 128;          // K elements (and bytes a row) per stage
@@ -125,25 +130,6 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr)
                  : "r"(cluster_addr)
                  : "memory");
     return v;
-}
-
-template <bool HALF>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi)
-{
-    if constexpr (HALF) {
-        uint32_t r;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-        return r;
-    } else {
-        return pack_bf16x2(lo, hi);
-    }
-}
-
-// The scaled result of one sum; the token's scale first, so that the sum
-// leaves the integer range before the channel's scale and bias are applied.
-__device__ __forceinline__ float scaled(int acc, float sa, float sb, float bias)
-{
-    return __fmaf_rn(__fmul_rn(__int2float_rn(acc), sa), sb, bias);
 }
 
 // Inclusive prefix sum / maximum over the lanes of a warp.
@@ -1199,6 +1185,7 @@ Choice choose(const Int8GemmArgs& a, int kernel, int sm_count)
 
 cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo& dev, cudaStream_t s)
 {
+    if (kernel != FP4_GEMM_PREFILL && gemv_int8_applies(a)) return launch_gemv_int8(a, dev, s);
     const Choice c = choose(a, kernel, dev.sm_count);
     if (c.swap) {
         const int64_t clusters = most_token_tiles(a, c.nt) * ((a.N + I8_BM - 1) / I8_BM);

@@ -456,9 +456,10 @@ fp4_status fp4_quantize_int8(const void* in, fp4_dtype in_dtype, int64_t rows_in
  *       between N and ldd are not written
  *   kernel : FP4_GEMM_PREFILL: CTA pairs, tiles of 256 channels x 32 to 256
  *       tokens; FP4_GEMM_DECODE: tiles of 128 channels x 16 to 128 tokens, K
- *       split over a cluster where the tiles are few; FP4_GEMM_AUTO: the one
- *       that takes less time by an estimate from the sizes.  Either takes any
- *       M, and both give the same bits.  FP4_GEMM_B_STATIC may be OR-ed: B is
+ *       split over a cluster where the tiles are few, or, for up to 8 tokens
+ *       and small weights, dot products without the tensor cores;
+ *       FP4_GEMM_AUTO: the one that takes less time by an estimate from the
+ *       sizes.  Each takes any M, and all give the same bits.  FP4_GEMM_B_STATIC may be OR-ed: B is
  *       not written by a kernel that may still be running on the stream when
  *       this one starts, so its first tiles are requested before that kernel
  *       has ended.

@@ -592,3 +592,27 @@ def test_grouped_captured_once_serves_any_routing(kernel):
                 check_product(d[s], a[s], sa[s], b[e], sb[e], None, (o, e))
                 d[s] = 5.0
         assert (d == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 1), (3, 15), (5, 16), (31, 17), (7, 511), (130, 512), (130, 513), (1000, 1536),
+                                 (33, 8191), (4, 40960), (9000, 70), (4097, 2049)])
+def test_few_tokens_small_weights(dtype, M, N, K):
+    # dot products and tensor cores on both sides of the choice between them
+    a, sa, b, sb, bias = operands(M, N, K, 31 * M + N, bias=N % 2 == 0)
+    b_end = torch.randint(-128, 128, (N, K), generator=torch.Generator().manual_seed(N), dtype=torch.int8).cuda()
+    ld = (K + 15) // 16 * 16
+    tight = torch.empty((N - 1) * ld + K, dtype=torch.int8, device="cuda").as_strided((N, K), (ld, 1))   # ends with its last code
+    tight.copy_(b_end)
+    for w in (b, tight):
+        got = []
+        for kernel in KERNELS + [fp4.GEMM_AUTO | fp4.GEMM_B_STATIC]:
+            whole = torch.full((M + 2, (N + 7) // 8 * 8 + 8), 3.0, dtype=dtype, device="cuda")
+            d = whole[1:M + 1, :N]
+            fp4.fp4_gemm_int8(a, sa, w, sb, d, bias, kernel)
+            got.append(d.clone())
+            d.fill_(3.0)
+            assert (whole == 3.0).all()
+        check_product(got[0], a, sa, w, sb, bias, (M, N, K))
+        assert all(torch.equal(g, got[0]) for g in got)
