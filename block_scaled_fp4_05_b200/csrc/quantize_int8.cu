@@ -140,7 +140,7 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int cols)
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (k + i < cols) w[i >> 1] |= (uint32_t)__ldg(row + k + i) << (16 * (i & 1));
+        if (k + i < cols) w[i >> 1] |= (uint32_t)__ldcg(row + k + i) << (16 * (i & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -185,10 +185,13 @@ struct QuantArgs {
 template <bool HALF, int TPR, int CH, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const QuantArgs p)
 {
-    // The next kernel may start its set-up; this one starts before the one
-    // before it has ended (0.5 us a launch) and touches nothing until then.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // This kernel starts before the one before it has ended (0.5 us a launch)
+    // and touches nothing until then.  Only then may the next one start its
+    // set-up: with the other order a product of static weights could request
+    // them while the kernel before this one still writes them (a weight
+    // quantized right before the layer's activation).
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int ROWS = THREADS / TPR;
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;

@@ -423,6 +423,25 @@ def test_chain_without_waits():
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M,N,K", [(16, 1024, 65536), (1, 400, 40000), (600, 1024, 65536)])
+def test_linear_right_after_its_weight_is_quantized(M, N, K):
+    # the weight's quantizer still runs when the layer is called, and the
+    # weight's memory holds another weight's codes until then
+    g = torch.Generator().manual_seed(16)
+    ws = [torch.randn(N, K, generator=g).to(BF).cuda() for _ in range(2)]
+    x = torch.randn(M, K, generator=g).to(BF).cuda()
+    want = []
+    for w in ws:
+        q = fp4.quantize_int8(w)
+        torch.cuda.synchronize()
+        want.append(fp4.linear_int8(x, *q))
+        torch.cuda.synchronize()
+    codes, scales = torch.empty(N, K, dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    for i in range(10):
+        fp4.fp4_quantize_int8(ws[i % 2], codes, scales)
+        assert torch.equal(fp4.linear_int8(x, codes, scales), want[i % 2])
+
+
 def test_bound_calls():
     a, sa, b, sb, bias = operands(20, 100, 200, 15, True)
     d = torch.zeros(20, 104, dtype=BF, device="cuda")[:, :100]
