@@ -615,7 +615,7 @@ static fp4_status gemm_int8(const void* A, int64_t lda, const float* sA, const v
     if (lda >= kMaxMapStride || ldb >= kMaxMapStride || stride_b >= kMaxMapStride || ldd >= kMaxMapStride / 2)
         return FP4_ERR_UNSUPPORTED_SHAPE;
     if (E == 1) stride_b = ldb;   // not used
-    else if (stride_b < (N - 1) * ldb + K) return FP4_ERR_INVALID_ARG;   // experts would overlap
+    else if (stride_b < (__int128)(N - 1) * ldb + K) return FP4_ERR_INVALID_ARG;   // experts would overlap
     if (lda % 16 != 0 || ldb % 16 != 0 || stride_b % 16 != 0 || ldd % 8 != 0 || !aligned16(A) || !aligned16(B) ||
         !aligned16(D) || !aligned4(sA) || !aligned4(sB) || !aligned4(bias) || !aligned4(offsets))
         return FP4_ERR_MISALIGNED;

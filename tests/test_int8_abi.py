@@ -152,3 +152,10 @@ def test_every_row_is_in_one_tile_and_the_bound_on_tiles_holds(nt):
             inside[first:end] = True
         assert (seen[inside] == 1).all() and (seen[~inside] == 0).all()
         assert listed <= M // nt + min(E, M)   # what the launch provides for
+
+
+def test_a_stride_too_small_by_more_than_64_bits_is_refused():
+    # (N - 1) * ldb leaves 64 bits: wrapped around it would be negative
+    N = 1 << 30
+    assert fp4.lib().fp4_gemm_int8_grouped(A16, 64, A16, A16, 1 << 39, 1 << 39, A16, A16, 2, 4, N, 64, None, 0, A16, N,
+                                           0, None) == 1
