@@ -194,7 +194,6 @@ struct SwapCfg {
     // before the stages: barriers, sA of the tokens, sB and bias of the channels
     static constexpr int OFF_SCALE = 256;
     static constexpr int FIXED = (OFF_SCALE + (NT + 2 * I8_BM) * 4 + 1023) / 1024 * 1024;
-    static constexpr int MIN_STAGES = (NT * I8_BM * 4 + STAGE_BYTES - 1) / STAGE_BYTES;   // the sums reuse their memory
     static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
     static constexpr int smem(int stages) { return 1024 + FIXED + stages * STAGE_BYTES; }
     static_assert((2 * MAX_STAGES + 1) * 8 + 40 <= OFF_SCALE, "barrier area");
@@ -968,22 +967,79 @@ I8Params params_of(const Int8GemmArgs& a, int bn)
     return p;
 }
 
+// How many clusters of the few-token kernel run at once with one, two or three
+// CTAs an SM (its share of the shared memory each).  Clusters do not cross the
+// SMs' groups (GPCs), whose sizes are no multiples of 4 or 8 and differ from
+// one GPU to the next: 148 SMs hold 15 clusters of 8 at a CTA each, not 18.
+struct Held {
+    int n[4][3];   // by log2 of the cluster's size and CTAs an SM
+    int of(int split, int ctas) const { return n[split >= 8 ? 3 : split >= 4 ? 2 : split - 1][ctas - 1]; }
+};
+
+// The occupancy query counts one CTA an SM for any kernel with tensor memory,
+// so it is asked about this one, which is never launched.
+__global__ void __launch_bounds__(kSwapThreads) occupancy_stand_in() {}
+
+Held query_held(int sm_count)
+{
+    Held h;
+    static uint64_t done = 0;
+    const void* kern = reinterpret_cast<const void*>(occupancy_stand_in);
+    for (int i = 0; i < 12; ++i) {
+        const int split = 1 << (i / 3), ctas = i % 3 + 1;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        launch_config(cfg, attr, (unsigned)(split * sm_count * ctas), kSwapThreads, (unsigned)split,
+                      (size_t)(kSmSmem / ctas - 1024), nullptr);
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (raise_smem(kern, kMaxSmem, done) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = sm_count * ctas / split;   // (only a launch's speed hangs on it)
+        }
+        h.n[i / 3][i % 3] = n;
+    }
+    return h;
+}
+
+// Of the current device, asked once.
+Held held_clusters(int sm_count)
+{
+    static std::mutex mu;
+    static Held known[64];
+    static uint64_t have = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return query_held(sm_count);
+    std::lock_guard<std::mutex> lock(mu);
+    if (!((have >> dev) & 1ull)) {
+        known[dev] = query_held(sm_count);
+        have |= 1ull << dev;
+    }
+    return known[dev];
+}
+
+// CTAs an SM of a launch, the fewest that run all its clusters at once.
+int swap_ctas(int nt, int split, double clusters, const Held& held)
+{
+    int ctas = 1;
+    while (ctas < swap_resident(nt) && clusters > held.of(split, ctas)) ++ctas;
+    return ctas;
+}
+
 // Stages of the few-token kernel: those of a CTA's share of K, as far as they
 // fit beside the other CTAs of the SM.
-template <int NT>
-int swap_stages(unsigned grid, int share, int sm_count)
+constexpr int swap_stages(int nt, int ctas, int share)
 {
-    using C = SwapCfg<NT>;
-    int ctas = (int)((grid + sm_count - 1) / sm_count);
-    if (ctas > swap_resident(NT)) ctas = swap_resident(NT);
-    const int room = (kSmSmem / ctas - 1024 - C::smem(0)) / C::STAGE_BYTES;
-    int n = share < room ? share : room;
-    if (n > C::MAX_STAGES) n = C::MAX_STAGES;
-    return n < C::MIN_STAGES ? C::MIN_STAGES : n;
+    const int bytes = I8_TILE + nt * I8_BK, fixed = 1024 + SwapCfg<128>::FIXED;
+    const int room = (kSmSmem / ctas - 1024 - fixed) / bytes;
+    const int least = (nt * I8_BM * 4 + bytes - 1) / bytes;   // the sums take their memory
+    const int n = share < room ? share : room;
+    return n < least ? least : n > SwapCfg<128>::MAX_STAGES ? SwapCfg<128>::MAX_STAGES : n;
 }
 
 template <int NT, bool HALF>
-cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, int sm_count, cudaStream_t s)
+cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, const Held& held, cudaStream_t s)
 {
     using C = SwapCfg<NT>;
     CUtensorMap tw = {}, tx = {};
@@ -999,10 +1055,10 @@ cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, int 
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         // as many clusters as the SMs hold take all tiles in turn
-        const int64_t hold = (int64_t)swap_resident(NT) * sm_count / split;
+        const int64_t hold = held.of(split, swap_resident(NT));
         const unsigned grid = (unsigned)((clusters < hold ? clusters : hold) * split);
         I8Params p = params_of(a, I8_BM);
-        p.stages = swap_stages<NT>(grid, (p.ks_total + split - 1) / split, sm_count);
+        p.stages = swap_stages(NT, swap_ctas(NT, split, (double)clusters, held), (p.ks_total + split - 1) / split);
         launch_config(cfg, attr, grid, kSwapThreads, (unsigned)split, C::smem(p.stages), s);
         e = cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
     }
@@ -1048,10 +1104,10 @@ cudaError_t launch_pair(const Int8GemmArgs& a, int bt, int64_t tiles, int sm_cou
 }
 
 template <int NT>
-cudaError_t launch_swap_t(const Int8GemmArgs& a, int split, int64_t clusters, int sm_count, cudaStream_t s)
+cudaError_t launch_swap_t(const Int8GemmArgs& a, int split, int64_t clusters, const Held& held, cudaStream_t s)
 {
-    return a.half_out ? launch_swap<NT, true>(a, split, clusters, sm_count, s)
-                      : launch_swap<NT, false>(a, split, clusters, sm_count, s);
+    return a.half_out ? launch_swap<NT, true>(a, split, clusters, held, s)
+                      : launch_swap<NT, false>(a, split, clusters, held, s);
 }
 
 cudaError_t launch_pair_t(const Int8GemmArgs& a, int bt, int64_t tiles, int sm_count, cudaStream_t s)
@@ -1142,7 +1198,7 @@ struct Choice {
     int nt, split, bt;
 };
 
-Choice choose(const Int8GemmArgs& a, int kernel, int sm_count)
+Choice choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
 {
     const int64_t ks = (a.K + I8_BK - 1) / I8_BK, tiles_n = (a.N + I8_BM - 1) / I8_BM;
     const Groups g = groups_of(a);
@@ -1153,7 +1209,7 @@ Choice choose(const Int8GemmArgs& a, int kernel, int sm_count)
         for (int i = 0; i < g.kinds; ++i) tiles += g.share[i] * std::ceil(g.rows[i] / nt);
         tiles *= g.count * tiles_n;
         for (int split = 1; split <= 8; split *= 2) {
-            if (split > 1 && (split > ks || tiles * split > swap_resident(nt) * sm_count)) break;
+            if (split > 1 && (split > ks || tiles > held.of(split, swap_resident(nt)))) break;
             const double us = swap_us(nt, split, tiles, ks, sm_count);
             // (a wider tile only for a clear gain: 16x4096x4096 takes 16
             // tokens 5.4, 32 6.1 us)
@@ -1186,13 +1242,14 @@ Choice choose(const Int8GemmArgs& a, int kernel, int sm_count)
 cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo& dev, cudaStream_t s)
 {
     if (kernel != FP4_GEMM_PREFILL && gemv_int8_applies(a)) return launch_gemv_int8(a, dev, s);
-    const Choice c = choose(a, kernel, dev.sm_count);
+    const Held held = held_clusters(dev.sm_count);
+    const Choice c = choose(a, kernel, held, dev.sm_count);
     if (c.swap) {
         const int64_t clusters = most_token_tiles(a, c.nt) * ((a.N + I8_BM - 1) / I8_BM);
-        if (c.nt == 16) return launch_swap_t<16>(a, c.split, clusters, dev.sm_count, s);
-        if (c.nt == 32) return launch_swap_t<32>(a, c.split, clusters, dev.sm_count, s);
-        if (c.nt == 64) return launch_swap_t<64>(a, c.split, clusters, dev.sm_count, s);
-        return launch_swap_t<128>(a, c.split, clusters, dev.sm_count, s);
+        if (c.nt == 16) return launch_swap_t<16>(a, c.split, clusters, held, s);
+        if (c.nt == 32) return launch_swap_t<32>(a, c.split, clusters, held, s);
+        if (c.nt == 64) return launch_swap_t<64>(a, c.split, clusters, held, s);
+        return launch_swap_t<128>(a, c.split, clusters, held, s);
     }
     return launch_pair_t(a, c.bt, most_token_tiles(a, c.bt) * ((a.N + 255) / 256), dev.sm_count, s);
 }
