@@ -122,6 +122,21 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_
         : "memory");
 }
 
+// One thread of a converged warp, the same one each time.  Unlike a test of
+// the lane it tells the compiler that a single thread runs the branch, whose
+// tensor-memory and TMA instructions take their operands from uniform
+// registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 __device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr)
 {
     int4 v;
@@ -367,7 +382,7 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         const int ntok = min(NT, rows - tm * NT);
 
         if (warp == 0) {
-            if (lane == 0) {
+            if (elect_one()) {
                 bool ok = true;
                 for (int ks = kb; ks < ke; ++ks) {
                     const uint32_t st = smem0 + stage * C::STAGE_BYTES;
@@ -395,7 +410,7 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             }
             __syncwarp();
         } else if (warp == 1) {
-            if (lane == 0 && kb < ke) {
+            if (kb < ke && elect_one()) {
                 const uint64_t adesc0 = desc_sw128(smem0);
                 const uint64_t bdesc0 = desc_sw128(smem0 + C::OFF_T);
                 for (int ks = kb; ks < ke; ++ks) {
@@ -666,7 +681,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     };
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmX.q[3])) : "memory");
             auto box = [&](const Place& w) { return (w.width * 4 + p.bt - 1) / p.bt; };   // quarters
@@ -725,7 +740,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 const uint32_t idesc = idesc_i8(256, width);
                 for (int ks = 0; ks < p.ks_total; ++ks) {
                     named_bar_sync(1 + stage, 64);
-                    if (lane == 0) {
+                    if (elect_one()) {
                         tc_fence_after();
                         const uint64_t step = (uint64_t)((uint32_t)stage * (stage_bytes >> 4));
 #pragma unroll
@@ -737,11 +752,11 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                     __syncwarp();
                     if (++stage == stages) stage = 0;
                 }
-                if (lane == 0) tc_commit_pair_both(ACC_FULL(buf));
+                if (elect_one()) tc_commit_pair_both(ACC_FULL(buf));
                 __syncwarp();
                 buf ^= 1;
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 // every pair MMA issued here has completed before the TMEM is freed
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain)
                              : "memory");
