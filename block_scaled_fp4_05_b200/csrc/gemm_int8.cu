@@ -1143,27 +1143,35 @@ int64_t most_token_tiles(const Int8GemmArgs& a, int nt)
 }
 
 // Estimated microseconds of a product, to choose a kernel and its tile by.
-// Both are bound by what an SM takes in: 107 KB a microsecond at most, less
-// with less of it in flight (a ring of stages turns over in 1.3 us or more).
-// Fitted to times on a B200 over M = 1..8192, N = 320..57344, K = 300..8192,
-// which they meet within about 15 % where HBM does not bind.
-//
-// Few tokens: `tiles` tiles of 128 channels x nt tokens, K split S ways.  The
-// split costs its join, which grows with the tokens.  16x4096x4096: S = 1
-// 12.2, 2 8.6, 4 6.5, 8 6.8 us; 64x4096x4096: 64 tokens S = 1 13.3, 4 8.3,
-// 32 tokens S = 4 7.8 us; 16x28672x8192: S = 1 40.6, 2 45 us.
-double swap_us(int nt, int split, double tiles, int64_t ks, int sm_count)
+// Fitted to times on a B200 (N of 64 to 28672, K of 104 to 14336, M = 7..829,
+// weights from memory), which they meet within 8 % in the mean; what they
+// choose takes 1.3 % longer there than the best choice, 1.19 times at most.
+double either(double a, double b) { return std::sqrt(std::sqrt(a * a * a * a + b * b * b * b)); }   // the larger, or a bit more
+double memory_us(double mb) { return mb / 6.4; }
+
+// Few tokens: `tiles` tiles of 128 channels x nt tokens, `tokens` of them
+// there, K split S ways.  A CTA takes a stage in 0.15 us at best and turns to
+// its next tile in 0.9 us or more (2.5 with offsets to search), the CTAs of an
+// SM together take 150 KB a microsecond, less where long rows start off a
+// 128-byte line (`ragged`: 1, else 0).  The split costs its join, which grows
+// with the tokens.  16x4096x4096: S = 1 8.4, 2 5.9, 4 6.4, 8 6.5 us;
+// 64x4096x4096: 64 tokens S = 2 6.9, 32 tokens S = 4 7.4 us.
+double swap_us(int nt, int split, double tiles, double tokens, int64_t ks, double mb, double ragged, bool grouped,
+               const Held& held)
 {
-    const double resident = swap_resident(nt);
-    const double ring_kb = nt == 16 ? 72 : nt == 32 ? 100 : 96;
-    const double kb = (double)((ks + split - 1) / split) * (I8_BM + nt) / 8;   // a CTA's operands
-    const double fixed = split == 1   ? 1.7 + 0.010 * nt
-                         : split == 2 ? 2.7 + 0.023 * nt
-                         : split == 4 ? 3.1 + 0.030 * nt
-                                      : 4.1 + 0.044 * nt;
-    const double n = tiles * split / sm_count;   // CTAs an SM
-    if (n <= resident) return fixed + kb / std::fmin(ring_kb / 1.3, 107.0 / std::ceil(n));
-    return 1.15 * n / resident * (fixed + kb / std::fmin(ring_kb / 1.3, 107.0 / resident));
+    const int ctas = swap_ctas(nt, split, tiles, held);
+    const double at_once = held.of(split, ctas), share = (double)((ks + split - 1) / split);
+    const double rounds = std::ceil(tiles / at_once - 1e-6);
+    const double join = tokens * (1 + 0.26 * (ctas - 1)), sms = std::fmin(tiles, at_once) / held.of(1, 1);
+    const double fixed = split == 1   ? 1.81 + 0.017 * join + 0.5 * sms
+                         : split == 2 ? 2.30 + 0.019 * join + 1.7 * sms
+                         : split == 4 ? 2.40 + 0.025 * join + 3.5 * sms
+                                      : 2.46 + 0.035 * join + 6.9 * sms;
+    // (rows past A are not loaded, the next expert's are)
+    const double intake = rounds * share * ctas * (I8_BM + (grouped ? nt : tokens)) / 8 / 150 *
+                          (1 + 0.8 * ragged * std::fmin(1, ks / 32.0));
+    const double steps = rounds * share * 0.15 + (rounds - 1) * ((grouped ? 2.5 : 0.9) + 0.032 * tokens);
+    return fixed + either(either(intake, steps), memory_us(mb));
 }
 
 // The groups of rows of a launch, as far as the host knows them: one, or some
@@ -1183,29 +1191,32 @@ Groups groups_of(const Int8GemmArgs& a)
 }
 
 // Many tokens: tiles of 256 channels x bt tokens on the CTA pairs, the last of
-// each group as narrow as its rows allow.  A stage takes 0.53 ns x (400 +
+// each group as narrow as its rows allow.  A stage takes 0.45 ns x (330 +
 // width): the tensor pipe's time is proportional to the width, the loads' is
-// not.  301x5003x4099: bt = 128 14.0, 160 14.9, 256 17.1 us; 1024x8192x8192:
-// 256 49.6, 192 59.8 us; 7680 rows over 128 experts of 2283x896: 192 55.5, 256
-// 57.9, 128 62.5 us.
-double pair_us(int bt, const Groups& g, int64_t N, int64_t ks, int sm_count)
+// not.  A tile's epilogue takes longer than the next tile's stages where K is
+// short.  301x5003x4099: bt = 128 13.5, 160 14.5, 256 16.7 us; 1024x8192x8192:
+// 256 52.9, 192 59.8 us; 7680 rows over 128 experts of 2283x896: 160 52.4, 192
+// 56.8, 128 57.5 us.
+double pair_us(int bt, const Groups& g, int64_t N, int64_t ks, double mb, double ragged, int sm_count)
 {
     const double pairs = sm_count / 2, tiles_n = (double)((N + 255) / 256);
     double tiles = 0, columns = 0, widest = 0;
     for (int i = 0; i < g.kinds; ++i) {
         const double whole = std::floor(g.rows[i] / bt), rest = std::ceil((g.rows[i] - whole * bt) / 32) * 32;
         tiles += g.share[i] * (whole + (rest > 0 ? 1 : 0));
-        columns += g.share[i] * (whole * (400 + bt) + (rest > 0 ? 400 + rest : 0));
-        widest = std::fmax(widest, 400 + (whole > 0 ? bt : rest));
+        columns += g.share[i] * (whole * (330 + bt) + (rest > 0 ? 330 + rest : 0));
+        widest = std::fmax(widest, whole > 0 ? bt : rest);
     }
     tiles *= g.count * tiles_n;
     columns *= g.count * tiles_n;
-    double longest = widest;   // of a pair
+    double longest = 330 + widest;   // of a pair
     if (tiles > pairs) {
         const double full = std::floor(tiles / pairs), rem = tiles - full * pairs;
-        longest = full * columns / tiles + (rem == 0 ? 0 : 2 * rem <= pairs ? 400 + bt / 2 : widest);
+        longest = full * columns / tiles + (rem == 0 ? 0 : 2 * rem <= pairs ? 330 + bt / 2 : 330 + widest);
     }
-    return 3.4 + 0.0085 * bt + 0.00053 * longest * ks;
+    const double products = 0.00045 * longest * ks * (1 + 0.27 * ragged);
+    const double epilogues = (std::ceil(tiles / pairs - 1e-6) - 1) * (1.05 + 0.0092 * (columns / tiles - 330));
+    return 2.06 + 0.0104 * widest + 1.6 * std::fmin(1, tiles / pairs) + either(either(products, epilogues), memory_us(mb));
 }
 
 struct Choice {
@@ -1217,18 +1228,22 @@ Choice choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
 {
     const int64_t ks = (a.K + I8_BK - 1) / I8_BK, tiles_n = (a.N + I8_BM - 1) / I8_BM;
     const Groups g = groups_of(a);
+    const double ragged = a.ldb % 128 != 0 ? 1 : 0;
+    // (experts: some have no rows, and their weights are not read)
+    const double mb = 1e-6 * ((a.offsets ? 0.8 : 1) * g.count * (double)a.N * (double)a.K + 2.0 * a.M * a.N);
+    double rows = 0;
+    for (int i = 0; i < g.kinds; ++i) rows += g.share[i] * g.rows[i];
     Choice c = {true, 128, 1, 256};
     double best_swap = 1e30, best_pair = 1e30;
     for (int nt = 16; nt <= 128; nt *= 2) {
-        double tiles = 0;
-        for (int i = 0; i < g.kinds; ++i) tiles += g.share[i] * std::ceil(g.rows[i] / nt);
-        tiles *= g.count * tiles_n;
+        double groups = 0;   // token tiles of a group, in the mean
+        for (int i = 0; i < g.kinds; ++i) groups += g.share[i] * std::ceil(g.rows[i] / nt);
+        const double tiles = groups * g.count * tiles_n;
         for (int split = 1; split <= 8; split *= 2) {
             if (split > 1 && (split > ks || tiles > held.of(split, swap_resident(nt)))) break;
-            const double us = swap_us(nt, split, tiles, ks, sm_count);
-            // (a wider tile only for a clear gain: 16x4096x4096 takes 16
-            // tokens 5.4, 32 6.1 us)
-            if (us < (nt == c.nt ? 1.0 : 0.93) * best_swap) {
+            const double us = swap_us(nt, split, tiles, rows / groups, ks, mb, ragged, a.offsets != nullptr, held);
+            // (a wider tile only for a gain)
+            if (us < (nt == c.nt ? 1.0 : 0.94) * best_swap) {
                 best_swap = us;
                 c.nt = nt;
                 c.split = split;
@@ -1236,18 +1251,12 @@ Choice choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
         }
     }
     for (int bt = 256; bt >= 32; bt -= 32) {
-        const double us = pair_us(bt, g, a.N, ks, sm_count);
-        if (us < best_pair) {
+        const double us = pair_us(bt, g, a.N, ks, mb, ragged, sm_count);
+        if (us <= best_pair) {   // (of equal ones the narrowest: more stages fit)
             best_pair = us;
             c.bt = bt;
         }
     }
-    // Where the weights' bytes bind, the few-token kernel reads them at 5.8
-    // TB/s or more and the pair kernel at 5.4 (64 experts of 2056x2048, 1031
-    // rows: 48 against 52 us).
-    const double weight_mb = 1e-6 * g.count * (double)a.N * (double)a.K;
-    best_swap = std::fmax(best_swap, weight_mb / 5.8 + 2);
-    best_pair = std::fmax(best_pair, weight_mb / 5.4 + 3);
     c.swap = kernel == FP4_GEMM_DECODE || a.K == 0 || (kernel == FP4_GEMM_AUTO && best_swap <= best_pair);
     return c;
 }
