@@ -1,8 +1,9 @@
 """Block-scaled FP4 (NVFP4 / MXFP4) quantization and W4A4 GEMM for B200.
 
 The compute lives in ``libfp4.so`` (hand-written sm_100a CUDA behind the C ABI
-of ``include/fp4.h``); ``fp4`` is its ctypes binding and ``synth`` the seeded
-input generator used by tests and benchmarks.
+of ``include/fp4.h``); ``fp4`` is its ctypes binding (the INT8 layers' calls go
+through the extension module ``_int8_calls``) and ``synth`` the seeded input
+generator used by tests and benchmarks.
 """
 from .fp4 import (  # noqa: F401
     NVFP4, MXFP4, ROWWISE, COLWISE, GEMM_AUTO, GEMM_PREFILL, GEMM_DECODE, Fp4Error,

@@ -546,7 +546,8 @@ def linear_int8(x, W, sW, bias=None, out=None, stream=None):
     """x W^T + bias for a bf16 or fp16 activation x and a weight quantized ahead
     of time by quantize_int8: the activation is quantized by token, then
     multiplied; the result has x's type unless `out` is given.  The product
-    starts loading the weight while the quantizer still runs."""
+    starts loading the weight while the activation's quantizer still runs; the
+    weight's own may be the call right before."""
     with _on(stream):
         codes, scales = quantize_int8(x)
         return gemm_int8(codes, scales, W, sW, bias, out, x.dtype, GEMM_AUTO | GEMM_B_STATIC)
