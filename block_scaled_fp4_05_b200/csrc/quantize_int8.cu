@@ -287,8 +287,12 @@ cudaError_t dispatch(const QuantArgs& p, cudaStream_t s)
     // Then a block a row.  Many rows: more chunks a thread, so that more bytes
     // are in flight (8192 rows of 8192: 8 chunks 33.2, 4 33.9, 2 42.3 us; 8194
     // of 4096: 4 17.8, 2 20.9).  Few: more threads (one row of 4096: 2 chunks
-    // 1.8, 4 2.1, 8 2.5 us; of 8192: 4 chunks 2.1, 8 2.6).
+    // 1.8, 4 2.1, 8 2.5 us; of 8192: 4 chunks 2.1, 8 2.6).  Gathered rows come
+    // from L2 in part, and then the reductions' instructions count: half as
+    // many threads (8194 rows of 4096 from 4097 17.0 -> 15.9 us, 4000 from 2000
+    // 7.0 -> 6.5; 2000 from 1000 4.1 -> 4.3; in order 16.3 -> 16.6).
     const bool many = p.rows > 1024;
+    if (p.cols <= 4096 && p.index && p.rows > 3000) return launch<HALF, 64, 8, 64>(p, s);
     if (p.cols <= 4096) return many ? launch<HALF, 128, 4, 128>(p, s) : launch<HALF, 256, 2, 256>(p, s);
     if (p.cols <= 8192) return many ? launch<HALF, 128, 8, 128>(p, s) : launch<HALF, 256, 4, 256>(p, s);
     if (p.cols <= 16384) return launch<HALF, 256, 8, 256>(p, s);

@@ -139,6 +139,21 @@ def test_quantize_gathers_rows(dtype, cols):
     check_quantized(x[index[kept.cuda()].long()], codes[kept.cuda()], scales[kept.cuda()])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("cols", [2049, 2600, 4090, 4096])
+def test_quantize_gathers_many_rows(dtype, cols):
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(400, (cols + 7) // 8 * 8, generator=g).to(dtype).cuda()[:, :cols]
+    x[17], x[18, cols - 1], x[19, 1] = 0, float("inf"), float("nan")
+    index = torch.randint(0, 400, (3101,), generator=g, dtype=torch.int32).cuda()
+    index[:6] = torch.tensor([17, 18, 19, -1, 400, 2 ** 31 - 1], dtype=torch.int32)
+    codes, scales = fp4.quantize_int8(x, index)
+    assert (codes[:6] == 0).all()
+    assert scales[0] == 1 and torch.isnan(scales[1:3]).all() and (scales[3:6] == 1).all()
+    kept = ((index >= 0) & (index < 400) & (index != 18) & (index != 19)).nonzero()[:, 0]
+    check_quantized(x[index[kept].long()], codes[kept], scales[kept])
+
+
 # ---------------------------------------------------------------------------
 # Products
 # ---------------------------------------------------------------------------
