@@ -12,6 +12,7 @@ p = |sum sA sB|, y = sum sA sB + bias and u the half step of the output type
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -420,6 +421,34 @@ def test_two_streams_at_once():
         check_product(d, a, sa, b, sb, None)
 
 
+def test_threads_with_streams_of_their_own():
+    g = torch.Generator().manual_seed(17)
+    jobs = []
+    for M, N, K in [(1, 300, 504), (20, 2056, 1496), (200, 900, 2048), (700, 600, 328)]:
+        w, sw = weights(g, 1, N, K)
+        x = torch.randn(M, (K + 7) // 8 * 8, generator=g).to(BF).cuda()[:, :K]
+        jobs.append((x, w[0], sw[0], fp4.linear_int8(x, w[0], sw[0]), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(x, w, sw, want, stream):
+        try:
+            for i in range(40):   # the stream as an object and as its handle
+                y = fp4.linear_int8(x, w, sw, stream=stream if i % 2 else stream.cuda_stream)
+                stream.synchronize()
+                if not torch.equal(y, want):
+                    wrong.append((tuple(x.shape), i))
+        except Exception as e:   # (an assertion of a thread is not seen by the test)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=job) for job in jobs * 2]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_chain_without_waits():
     # each product's output is the next one's input, nothing waits in between
     g = torch.Generator().manual_seed(14)
@@ -542,6 +571,7 @@ def test_expert_stride_is_no_multiple_of_the_rows(kernel):
 
 FIRST_CALL = """
 import sys
+import threading
 sys.path.insert(0, %r)
 import torch
 from block_scaled_fp4_05_b200 import fp4
