@@ -1065,7 +1065,8 @@ cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, cons
     }
     static uint64_t done = 0;
     auto kern = int8_swap_kernel<NT, HALF>;
-    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), C::smem(C::MAX_STAGES) < kMaxSmem ? C::smem(C::MAX_STAGES) : kMaxSmem, done);
+    constexpr int most = C::smem(C::MAX_STAGES) < kMaxSmem ? C::smem(C::MAX_STAGES) : kMaxSmem;
+    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), most, done);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
