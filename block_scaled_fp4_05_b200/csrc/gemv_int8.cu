@@ -39,10 +39,12 @@ struct GemvArgs {
     int M, N, K, ksplit, b_static;
 };
 
+// Not through the read-only path: weights that are not static may be written
+// by the kernel before, which can still be running when this one starts.
 __device__ __forceinline__ int4 ld_stream(const int8_t* p)
 {
     int4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.s32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;

@@ -24,6 +24,19 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p)
     return v;
 }
 
+// The same for what the kernel before may have written, where this one starts
+// before that one has ended: the read-only path of ld_stream wants data that
+// stay as they are for the reading kernel's whole life, and a wait inside the
+// kernel orders ordinary loads only.
+__device__ __forceinline__ uint4 ld_stream_coherent(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // Largest BF16 magnitude (sign cleared, as an integer) of 8 packed values.
 __device__ __forceinline__ uint32_t absmax8(uint4 v)
 {

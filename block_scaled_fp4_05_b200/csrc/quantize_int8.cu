@@ -136,7 +136,7 @@ __device__ __forceinline__ uint2 codes8(uint4 v, const RowScale& s, bool finite)
 // Elements [k, k + 8) of a row of `cols`; nothing behind the row is read.
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int cols)
 {
-    if (k + 8 <= cols) return qdev::ld_stream(reinterpret_cast<const uint4*>(row + k));
+    if (k + 8 <= cols) return qdev::ld_stream_coherent(reinterpret_cast<const uint4*>(row + k));
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const QuantArgs 
         for (int c = 0; c < CH; ++c) {
             const int k = (c * TPR + t) * 8;
             if (FULL && inside)
-                v[c] = qdev::ld_stream(reinterpret_cast<const uint4*>(x + k));
+                v[c] = qdev::ld_stream_coherent(reinterpret_cast<const uint4*>(x + k));
             else
                 v[c] = !FULL && k < cols ? load8(x, k, cols) : make_uint4(0u, 0u, 0u, 0u);
         }

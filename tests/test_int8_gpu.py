@@ -680,3 +680,51 @@ def test_few_tokens_small_weights(dtype, M, N, K):
             assert (whole == 3.0).all()
         check_product(got[0], a, sa, w, sb, bias, (M, N, K))
         assert all(torch.equal(g, got[0]) for g in got)
+
+
+# ---------------------------------------------------------------------------
+# Operands that the call right before writes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("M", [1, 4, 8, 20])
+def test_product_right_after_its_weight_is_rewritten(M):
+    # no B_STATIC: the weight's quantizer may be the kernel before, and the
+    # weight's memory has been read with other codes in it by the call before that
+    g = torch.Generator().manual_seed(40 + M)
+    N, K = 480, 2000
+    ws = [torch.randn(N, K, generator=g).to(BF).cuda() for _ in range(2)]
+    a, sa = random_codes(g, M, K), torch.rand(M, generator=g).cuda()
+    want = []
+    for w in ws:
+        q = fp4.quantize_int8(w)
+        torch.cuda.synchronize()
+        want.append(fp4.gemm_int8(a, sa, *q))
+        check_product(want[-1], a, sa, *q, None)
+        torch.cuda.synchronize()
+    codes, scales = torch.empty(N, K, dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    got = []
+    for i in range(60):
+        fp4.fp4_quantize_int8(ws[i % 2], codes, scales)
+        got.append(fp4.gemm_int8(a, sa, codes, scales))
+    torch.cuda.synchronize()
+    assert all(torch.equal(d, want[i % 2]) for i, d in enumerate(got))
+
+
+@pytest.mark.parametrize("M,N", [(1, 1000), (8, 4096), (300, 2056)])
+def test_quantizer_right_after_its_input_is_rewritten(M, N):
+    g = torch.Generator().manual_seed(50 + M)
+    K = 512
+    b, sb = random_codes(g, N, K), torch.rand(N, generator=g).cuda()
+    inputs = [(random_codes(g, M, K), torch.rand(M, generator=g).cuda()) for _ in range(2)]
+    want = []
+    for a, sa in inputs:
+        d = fp4.gemm_int8(a, sa, b, sb)
+        torch.cuda.synchronize()
+        want.append(fp4.quantize_int8(d))
+        check_quantized(d, *want[-1])
+    d = torch.zeros(M, (N + 7) // 8 * 8, dtype=BF, device="cuda")[:, :N]
+    got = []
+    for i in range(60):
+        fp4.fp4_gemm_int8(*inputs[i % 2], b, sb, d)
+        got.append(fp4.quantize_int8(d))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[0], want[i % 2][0]) and torch.equal(g[1], want[i % 2][1]) for i, g in enumerate(got))
