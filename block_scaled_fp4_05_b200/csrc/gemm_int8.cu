@@ -402,9 +402,14 @@ int8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                         phase ^= 1u;
                     }
                 }
-                // Only now may the next kernel start: its first weight loads
-                // beside this one's cost more than they hid (1x28672x8192,
-                // call after call: 39.8 us, 48 with the trigger at the start).
+                // Once the first item's loads are issued the next kernel may
+                // start: before them, its first weight loads beside this
+                // one's cost more than they hid (1x28672x8192, call after
+                // call: 39.8 us, 48 with the trigger at the start).  Where a
+                // cluster takes several items in turn, waiting for the last
+                // one's gains nothing: 16x28672x1024 6.5 -> 6.7 us, 16 rows
+                // over 8 experts of 14336x4096 72 -> 76, 500 over 64 of
+                // 4096x1024 45.3 -> 44.7.
                 pdl_trigger();
                 if (!ok || *abort_flag) spin_ns(200000);   // loads in flight land before the memory is used again
             }

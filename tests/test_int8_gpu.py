@@ -728,3 +728,37 @@ def test_quantizer_right_after_its_input_is_rewritten(M, N):
         got.append(fp4.quantize_int8(d))
     torch.cuda.synchronize()
     assert all(torch.equal(g[0], want[i % 2][0]) and torch.equal(g[1], want[i % 2][1]) for i, g in enumerate(got))
+
+
+@pytest.mark.parametrize("experts", [0, 40])
+def test_few_token_launches_of_several_turns_right_behind_each_other(experts):
+    # more tiles than clusters run at once, each launch's weights written by the call before it
+    g = torch.Generator().manual_seed(60 + experts)
+    M, K = 48, 640
+    N = 2056 if experts else 60000
+    a, sa = random_codes(g, M, K), torch.rand(M, generator=g).cuda()
+    ws = [torch.randn((experts or 1) * N, K, generator=g).to(BF).cuda() for _ in range(2)]
+    off = torch.tensor(np.linspace(0, M, experts + 1).astype(int), dtype=torch.int32, device="cuda") if experts else None
+    codes, scales = torch.empty_like(ws[0], dtype=torch.int8), torch.empty(len(ws[0]), device="cuda")
+
+    def product():
+        if experts:
+            return fp4.gemm_int8_grouped(a, sa, codes.unflatten(0, (experts, N)), scales.view(experts, N), off,
+                                         kernel=fp4.GEMM_DECODE)
+        return fp4.gemm_int8(a, sa, codes, scales, kernel=fp4.GEMM_DECODE)
+
+    want = []
+    for w in ws:
+        fp4.fp4_quantize_int8(w, codes, scales)
+        torch.cuda.synchronize()
+        d = product()
+        for e in range(experts or 1):
+            rows = slice(*off[e:e + 2].tolist()) if experts else slice(None)
+            check_product(d[rows], a[rows], sa[rows], codes[e * N:(e + 1) * N], scales[e * N:(e + 1) * N], None)
+        want.append(d)
+    got = []
+    for i in range(12):
+        fp4.fp4_quantize_int8(ws[i % 2], codes, scales)
+        got += [product(), product()]
+    torch.cuda.synchronize()
+    assert all(torch.equal(d, want[i // 2 % 2]) for i, d in enumerate(got))
