@@ -591,12 +591,12 @@ fp4_status fp4_quantize_int8(const void* in, fp4_dtype in_dtype, int64_t rows_in
                                                scales_out, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// Shared part of the two INT8 products: M rows of A and D (all experts'
-// together in the grouped form).
+// Shared part of the INT8 products: M rows of A and D (all experts' together in
+// the grouped form); form: the one to compute by, or NULL.
 static fp4_status gemm_int8(const void* A, int64_t lda, const float* sA, const void* B, int64_t ldb,
                             int64_t stride_b, const float* sB, const int32_t* offsets, int64_t E, int64_t M,
                             int64_t N, int64_t K, const float* bias, fp4_dtype out_dtype, void* D, int64_t ldd,
-                            fp4_gemm_kernel kernel, fp4_stream_t stream)
+                            fp4_gemm_kernel kernel, fp4_stream_t stream, const fp4::Int8Form* form = nullptr)
 {
     const int flags = (int)kernel & ~0xFF;
     const int choice = (int)kernel & 0xFF;
@@ -619,10 +619,6 @@ static fp4_status gemm_int8(const void* A, int64_t lda, const float* sA, const v
     if (lda % 16 != 0 || ldb % 16 != 0 || stride_b % 16 != 0 || ldd % 8 != 0 || !aligned16(A) || !aligned16(B) ||
         !aligned16(D) || !aligned4(sA) || !aligned4(sB) || !aligned4(bias) || !aligned4(offsets))
         return FP4_ERR_MISALIGNED;
-    fp4::DeviceInfo dev;
-    fp4_status st = require_device(&dev);
-    if (st != FP4_OK) return st;
-    if (!fp4::tensor_map_encoder_available()) return FP4_ERR_NO_DEVICE;
     fp4::Int8GemmArgs a;
     a.A = static_cast<const int8_t*>(A);
     a.lda = lda;
@@ -641,7 +637,12 @@ static fp4_status gemm_int8(const void* A, int64_t lda, const float* sA, const v
     a.D = static_cast<uint16_t*>(D);
     a.ldd = ldd;
     a.b_static = (flags & FP4_GEMM_B_STATIC) != 0;
-    return from_cuda(fp4::launch_gemm_int8(a, choice, dev, reinterpret_cast<cudaStream_t>(stream)));
+    if (form && !fp4::int8_form_applies(a, *form)) return FP4_ERR_INVALID_ARG;
+    fp4::DeviceInfo dev;
+    fp4_status st = require_device(&dev);
+    if (st != FP4_OK) return st;
+    if (!fp4::tensor_map_encoder_available()) return FP4_ERR_NO_DEVICE;
+    return from_cuda(fp4::launch_gemm_int8(a, choice, form, dev, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 fp4_status fp4_gemm_int8(const void* A, int64_t lda, const float* sA, const void* B, int64_t ldb,
@@ -663,6 +664,20 @@ fp4_status fp4_gemm_int8_grouped(const void* A, int64_t lda, const float* sA, co
     if (E > 0 && T > 0 && N > 0 && !offsets) return FP4_ERR_INVALID_ARG;
     return gemm_int8(A, lda, sA, B, ldb, stride_b, sB, offsets, E, T, N, K, bias, out_dtype, D, ldd, kernel,
                      stream);
+}
+
+fp4_status fp4_selftest_gemm_int8(fp4_gemm_kernel kernel, int tile, int split, const void* A, int64_t lda,
+                                  const float* sA, const void* B, int64_t ldb, int64_t stride_b, const float* sB,
+                                  const int32_t* offsets, int64_t E, int64_t T, int64_t N, int64_t K,
+                                  const float* bias, fp4_dtype out_dtype, void* D, int64_t ldd, fp4_stream_t stream)
+{
+    fp4::g_last_error[0] = 0;
+    const int choice = (int)kernel & 0xFF;
+    if (E < 0 || stride_b < 0 || (!offsets && E != 1) || choice == FP4_GEMM_AUTO) return FP4_ERR_INVALID_ARG;
+    if (E > fp4::kInt8MaxExperts) return FP4_ERR_UNSUPPORTED_SHAPE;
+    const fp4::Int8Form form = {choice == FP4_GEMM_DECODE, tile, split};
+    return gemm_int8(A, lda, sA, B, ldb, stride_b, sB, offsets, E, T, N, K, bias, out_dtype, D, ldd, kernel, stream,
+                     &form);
 }
 
 fp4_status fp4_selftest_bounded_wait(fp4_stream_t stream)

@@ -116,7 +116,15 @@ struct Int8GemmArgs {
     int64_t ldd;
     bool b_static;
 };
-cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo& dev, cudaStream_t s);
+// How a product is computed: by the few-token kernel with tiles of `tile`
+// tokens and K split `split` ways, or by CTA pairs with tiles of up to `tile`.
+struct Int8Form {
+    bool swap;
+    int tile, split;
+};
+bool int8_form_applies(const Int8GemmArgs& a, const Int8Form& f);
+// form: NULL for the one that takes less time by an estimate
+cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const Int8Form* form, const DeviceInfo& dev, cudaStream_t s);
 // gemv_int8.cu: a few tokens and small weights
 bool gemv_int8_applies(const Int8GemmArgs& a);
 cudaError_t launch_gemv_int8(const Int8GemmArgs& a, const DeviceInfo& dev, cudaStream_t s);

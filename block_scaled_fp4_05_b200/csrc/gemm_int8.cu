@@ -1225,12 +1225,7 @@ double pair_us(int bt, const Groups& g, int64_t N, int64_t ks, double mb, double
     return 2.06 + 0.0104 * widest + 1.6 * std::fmin(1, tiles / pairs) + either(either(products, epilogues), memory_us(mb));
 }
 
-struct Choice {
-    bool swap;
-    int nt, split, bt;
-};
-
-Choice choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
+Int8Form choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
 {
     const int64_t ks = (a.K + I8_BK - 1) / I8_BK, tiles_n = (a.N + I8_BM - 1) / I8_BM;
     const Groups g = groups_of(a);
@@ -1239,7 +1234,7 @@ Choice choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
     const double mb = 1e-6 * ((a.offsets ? 0.8 : 1) * g.count * (double)a.N * (double)a.K + 2.0 * a.M * a.N);
     double rows = 0;
     for (int i = 0; i < g.kinds; ++i) rows += g.share[i] * g.rows[i];
-    Choice c = {true, 128, 1, 256};
+    Int8Form few = {true, 128, 1}, many = {false, 256, 1};
     double best_swap = 1e30, best_pair = 1e30;
     for (int nt = 16; nt <= 128; nt *= 2) {
         double groups = 0;   // token tiles of a group, in the mean
@@ -1249,10 +1244,10 @@ Choice choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
             if (split > 1 && (split > ks || tiles > held.of(split, swap_resident(nt)))) break;
             const double us = swap_us(nt, split, tiles, rows / groups, ks, mb, ragged, a.offsets != nullptr, held);
             // (a wider tile only for a gain)
-            if (us < (nt == c.nt ? 1.0 : 0.94) * best_swap) {
+            if (us < (nt == few.tile ? 1.0 : 0.94) * best_swap) {
                 best_swap = us;
-                c.nt = nt;
-                c.split = split;
+                few.tile = nt;
+                few.split = split;
             }
         }
     }
@@ -1260,28 +1255,38 @@ Choice choose(const Int8GemmArgs& a, int kernel, const Held& held, int sm_count)
         const double us = pair_us(bt, g, a.N, ks, mb, ragged, sm_count);
         if (us <= best_pair) {   // (of equal ones the narrowest: more stages fit)
             best_pair = us;
-            c.bt = bt;
+            many.tile = bt;
         }
     }
-    c.swap = kernel == FP4_GEMM_DECODE || a.K == 0 || (kernel == FP4_GEMM_AUTO && best_swap <= best_pair);
-    return c;
+    return kernel == FP4_GEMM_DECODE || a.K == 0 || (kernel == FP4_GEMM_AUTO && best_swap <= best_pair) ? few : many;
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const DeviceInfo& dev, cudaStream_t s)
+// Those that `choose` can return.
+bool int8_form_applies(const Int8GemmArgs& a, const Int8Form& f)
 {
-    if (kernel != FP4_GEMM_PREFILL && gemv_int8_applies(a)) return launch_gemv_int8(a, dev, s);
+    const int64_t ks = (a.K + I8_BK - 1) / I8_BK;
+    if (f.swap)
+        return (f.tile == 16 || f.tile == 32 || f.tile == 64 || f.tile == 128) &&
+               (f.split == 1 || ((f.split == 2 || f.split == 4 || f.split == 8) && f.split <= ks));
+    return f.tile >= 32 && f.tile <= 256 && f.tile % 32 == 0 && f.split == 1 && a.K > 0;
+}
+
+cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const Int8Form* form, const DeviceInfo& dev,
+                             cudaStream_t s)
+{
+    if (!form && kernel != FP4_GEMM_PREFILL && gemv_int8_applies(a)) return launch_gemv_int8(a, dev, s);
     const Held held = held_clusters(dev.sm_count);
-    const Choice c = choose(a, kernel, held, dev.sm_count);
-    if (c.swap) {
-        const int64_t clusters = most_token_tiles(a, c.nt) * ((a.N + I8_BM - 1) / I8_BM);
-        if (c.nt == 16) return launch_swap_t<16>(a, c.split, clusters, held, s);
-        if (c.nt == 32) return launch_swap_t<32>(a, c.split, clusters, held, s);
-        if (c.nt == 64) return launch_swap_t<64>(a, c.split, clusters, held, s);
-        return launch_swap_t<128>(a, c.split, clusters, held, s);
+    const Int8Form f = form ? *form : choose(a, kernel, held, dev.sm_count);
+    if (f.swap) {
+        const int64_t clusters = most_token_tiles(a, f.tile) * ((a.N + I8_BM - 1) / I8_BM);
+        if (f.tile == 16) return launch_swap_t<16>(a, f.split, clusters, held, s);
+        if (f.tile == 32) return launch_swap_t<32>(a, f.split, clusters, held, s);
+        if (f.tile == 64) return launch_swap_t<64>(a, f.split, clusters, held, s);
+        return launch_swap_t<128>(a, f.split, clusters, held, s);
     }
-    return launch_pair_t(a, c.bt, most_token_tiles(a, c.bt) * ((a.N + 255) / 256), dev.sm_count, s);
+    return launch_pair_t(a, f.tile, most_token_tiles(a, f.tile) * ((a.N + 255) / 256), dev.sm_count, s);
 }
 
 cudaError_t read_and_clear_int8_error_word(unsigned int* word)

@@ -100,6 +100,9 @@ def lib():
         L.fp4_gemm_int8_grouped.restype = c.c_int
         L.fp4_gemm_int8_grouped.argtypes = [P, i64, P, P, i64, i64, P, P, i64, i64, i64, i64, P, c.c_int, P,
                                             i64, c.c_int, st]
+        L.fp4_selftest_gemm_int8.restype = c.c_int
+        L.fp4_selftest_gemm_int8.argtypes = [c.c_int, c.c_int, c.c_int, P, i64, P, P, i64, i64, P, P, i64, i64, i64, i64,
+                                             P, c.c_int, P, i64, st]
         _lib = L
     return _lib
 
@@ -466,6 +469,17 @@ def fp4_get_device_status(stream=None):
 
 def fp4_selftest_bounded_wait(stream=None):
     _check(lib().fp4_selftest_bounded_wait(_stream(stream)), "fp4_selftest_bounded_wait")
+
+
+def fp4_selftest_gemm_int8(kernel, tile, split, A, sA, B, sB, D, offsets=None, bias=None, stream=None):
+    """fp4_gemm_int8, or fp4_gemm_int8_grouped with offsets, by the named form
+    (the tile's tokens and the split of K) instead of the chosen one."""
+    if offsets is None:
+        args = bind_gemm_int8(A, sA, B, sB, D, bias, kernel, stream)._args
+        args = args[:5] + (0, args[5], None, 1) + args[6:]
+    else:
+        args = bind_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias, kernel, stream)._args
+    _check(lib().fp4_selftest_gemm_int8(args[16], tile, split, *args[:16], args[17]), "fp4_selftest_gemm_int8")
 
 
 # ---------------------------------------------------------------------------

@@ -518,6 +518,22 @@ fp4_status fp4_get_device_status(fp4_stream_t stream);
  */
 fp4_status fp4_selftest_bounded_wait(fp4_stream_t stream);
 
+/*
+ * Self-test of the INT8 products: fp4_gemm_int8 (offsets NULL, E == 1) or
+ * fp4_gemm_int8_grouped by a named form instead of the one that the library
+ * would take, so that each can be checked at any size.
+ *   kernel : FP4_GEMM_PREFILL: CTA pairs with tiles of up to `tile` tokens, a
+ *       multiple of 32 up to 256; split == 1; K > 0.  FP4_GEMM_DECODE: tiles of
+ *       128 channels x `tile` tokens (16, 32, 64 or 128) with K split over
+ *       `split` CTAs (1, 2, 4 or 8, not more than K has pieces of 128).
+ *       FP4_GEMM_B_STATIC may be OR-ed.  Others: FP4_ERR_INVALID_ARG.
+ * All forms give the same bits.
+ */
+fp4_status fp4_selftest_gemm_int8(fp4_gemm_kernel kernel, int tile, int split, const void* A, int64_t lda,
+                                  const float* sA, const void* B, int64_t ldb, int64_t stride_b, const float* sB,
+                                  const int32_t* offsets, int64_t E, int64_t T, int64_t N, int64_t K,
+                                  const float* bias, fp4_dtype out_dtype, void* D, int64_t ldd, fp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

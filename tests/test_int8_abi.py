@@ -159,3 +159,75 @@ def test_a_stride_too_small_by_more_than_64_bits_is_refused():
     N = 1 << 30
     assert fp4.lib().fp4_gemm_int8_grouped(A16, 64, A16, A16, 1 << 39, 1 << 39, A16, A16, 2, 4, N, 64, None, 0, A16, N,
                                            0, None) == 1
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(kernel=0), 1), (dict(kernel=3), 1), (dict(kernel=1, tile=48), 1), (dict(kernel=1, tile=0), 1),
+    (dict(kernel=1, tile=288), 1), (dict(kernel=1, tile=64, split=2), 1), (dict(kernel=1, tile=64, K=0), 1),
+    (dict(kernel=2, tile=48), 1), (dict(kernel=2, tile=256), 1), (dict(kernel=2, split=3), 1), (dict(kernel=2, split=0), 1),
+    (dict(kernel=2, split=16, K=4096, lda=4096, ldb=4096), 1), (dict(kernel=2, split=2, K=128, lda=128, ldb=128), 1),
+    (dict(E=2), 1), (dict(E=-1), 1), (dict(stride=-16), 1), (dict(E=513, offsets=A16), 2), (dict(A=A1), 3), (dict(M=0), 0),
+    (dict(), 6), (dict(kernel=0x102), 6), (dict(kernel=1, tile=224), 6), (dict(kernel=2, split=2, K=129, lda=144, ldb=144), 6),
+    (dict(kernel=2, K=0), 6), (dict(E=2, offsets=A16, stride=1 << 20), 6),
+])
+def test_selftest_gemm_int8_refusals(change, want):
+    if want == 6 and not no_gpu():
+        pytest.skip("a device is present")
+    a = {**GOOD, "kernel": 2, "tile": 32, "split": 1, "offsets": None, "E": 1, "stride": 0, **change}
+    assert fp4.lib().fp4_selftest_gemm_int8(a["kernel"], a["tile"], a["split"], a["A"], a["lda"], a["sA"], a["B"], a["ldb"],
+                                            a["stride"], a["sB"], a["offsets"], a["E"], a["M"], a["N"], a["K"], a["bias"],
+                                            a["out"], a["D"], a["ldd"], None) == want
+
+
+# ---- the pair kernel's work items, restated: tiles, halves of the last wave,
+# token boxes and the epilogue's chunks ----
+def pair_items(bounds, tiles_n, bt, pairs, rg):
+    """(expert, row, row end, channel tile, width) of every item, as `locate` finds them."""
+    mts = [(end - first + bt - 1) // bt for first, end in bounds]
+    tiles = sum(mts) * tiles_n
+    rem = tiles % pairs
+    split_from = tiles - rem if 2 * rem <= pairs else tiles
+    for item in range(2 * tiles - split_from):
+        t, half, halved = item, 0, item >= split_from
+        if halved:
+            half, t = (item - split_from) & 1, split_from + (item - split_from) // 2
+        e = 0
+        while t >= mts[e] * tiles_n:
+            t -= mts[e] * tiles_n
+            e += 1
+        first, end = bounds[e]
+        group = min(rg, max(mts))
+        grp, within = divmod(t, group * tiles_n)
+        gm = min(mts[e] - grp * group, group)
+        row, col = first + (grp * group + within % gm) * bt, within // gm
+        width = min(bt, (end - row + 31) & ~31)
+        if halved:
+            upper = (width // 2 + 31) & ~31
+            row += half * upper
+            width = width - upper if half else upper
+        yield e, row, end, col, width
+
+
+@pytest.mark.parametrize("bt", range(32, 257, 32))
+def test_pair_items_cover_every_row_once_and_their_boxes_fit(bt):
+    rng = np.random.default_rng(bt)
+    for _ in range(40):
+        E, tiles_n = int(rng.integers(1, 9)), int(rng.integers(1, 30))
+        counts = rng.integers(0, 4 * bt, E) * (rng.random(E) < 0.8)
+        o = np.concatenate([[0], np.cumsum(counts)])
+        if o[-1] == 0:
+            continue
+        bounds = list(zip(o[:-1].tolist(), o[1:].tolist()))
+        most = int(o[-1] // bt + min(E, o[-1])) * tiles_n
+        seen = np.zeros((int(o[-1]), tiles_n), np.int64)
+        for e, row, end, col, width in pair_items(bounds, tiles_n, bt, min(most, 74), int(rng.integers(1, 9))):
+            if width == 0:
+                continue
+            assert width % 32 == 0 and 32 <= width <= bt        # what the pair MMA takes
+            box = (width * 4 + bt - 1) // bt                    # quarters of a CTA's share of the widest tile
+            assert 1 <= box <= 4 and width // 2 <= box * (bt // 8) <= bt // 2 and bt // 8 * box <= 256
+            chunks = [(width // 32 - half + 1) >> 1 for half in (0, 1)]
+            assert sorted(h + 2 * c for h in (0, 1) for c in range(chunks[h])) == list(range(width // 32)) and max(chunks) <= 4
+            seen[row:min(row + width, end), col] += 1
+        assert (seen == 1).all()
+        assert (bt // 2 * 128) % 1024 == 0                      # a stage's tiles start where the swizzle does

@@ -603,7 +603,7 @@ def test_first_calls_of_a_process_are_captured(M):
 
 
 # ---------------------------------------------------------------------------
-# Drawn sizes: every kernel, tile width and split that the choice reaches
+# Drawn sizes, by the forms that the choice takes for them
 # ---------------------------------------------------------------------------
 def drawn(seed, lo, hi):
     return int(round(np.exp(np.random.default_rng(seed).uniform(np.log(lo), np.log(hi)))))
@@ -762,3 +762,91 @@ def test_few_token_launches_of_several_turns_right_behind_each_other(experts):
         got += [product(), product()]
     torch.cuda.synchronize()
     assert all(torch.equal(d, want[i // 2 % 2]) for i, d in enumerate(got))
+
+
+# ---------------------------------------------------------------------------
+# Every form that the choice can take: tile widths and splits by name
+# ---------------------------------------------------------------------------
+PAIR = [(fp4.GEMM_PREFILL, bt, 1) for bt in range(32, 257, 32)]
+FEW = [(fp4.GEMM_DECODE, nt, split) for nt in (16, 32, 64, 128) for split in (1, 2, 4, 8)]
+
+
+def cta_pairs():
+    return torch.cuda.get_device_properties(0).multi_processor_count // 2
+
+
+def dense_by_form(form, M, N, K, dtype, seed, static=False, want=None):
+    kernel, tile, split = form
+    a, sa, b, sb, bias = operands(M, N, K, seed, True)
+    whole = torch.full((M + 2, (N + 7) // 8 * 8 + 8), 3.0, dtype=dtype, device="cuda")
+    d = whole[1:M + 1, :N]
+    fp4.fp4_selftest_gemm_int8(kernel | (fp4.GEMM_B_STATIC if static else 0), tile, split, a, sa, b, sb, d, bias=bias)
+    got = d.clone()
+    check_product(got, a, sa, b, sb, bias, (form, M, N, K))
+    assert torch.equal(got, fp4.gemm_int8(a, sa, b, sb, bias, out_dtype=dtype)), "other bits than the form that is chosen"
+    d.fill_(3.0)
+    assert (whole == 3.0).all(), "wrote outside D"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("form", PAIR, ids=str)
+def test_pair_form(form, dtype):
+    bt, pairs = form[1], cta_pairs()
+    # a remainder of tokens and channels, less than a wave, K longer than the ring
+    dense_by_form(form, bt + bt // 2 + 5, 300, 2500, dtype, bt)
+    dense_by_form(form, bt - 3, 264, 130, dtype, bt + 1, static=True)
+    # a wave and a few tiles more, which are computed as halves; the last token tile is narrow
+    dense_by_form(form, 3 * bt + bt // 2 + 3, (pairs // 4 + 2) * 256 - 20, 420, dtype, bt + 2)
+    # whole tiles only, a last wave too long for halves
+    dense_by_form(form, 4 * bt, ((pairs + pairs // 2) // 4 + 1) * 256, 384, dtype, bt + 3, static=True)
+    # several tiles a pair, a short K: both accumulators in turn
+    dense_by_form(form, 5 * bt + 1, (pairs // 2) * 256 + 8, 100, dtype, bt + 4)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("form", FEW, ids=str)
+def test_few_token_form(form, dtype):
+    nt, split = form[1:]
+    dense_by_form(form, 2 * nt + nt // 2 + 1, 434, 1300, dtype, nt + split)                # a CTA's shares of K differ
+    dense_by_form(form, nt, 130, 128 * split - 5, dtype, nt + split + 1, static=True)      # one stage a CTA
+    dense_by_form(form, nt - 3, 384, 128 * 13 * split + 40, dtype, nt + split + 2)         # more stages than the ring has
+    # more tiles than run at once, so clusters take them in turn
+    dense_by_form(form, 3 * nt - 1, 25650, 1050, dtype, nt + split + 3, static=True)
+
+
+def grouped_by_form(form, counts, N, K, dtype, seed, first=0, tail=0):
+    kernel, tile, split = form
+    offsets = ends(*counts, first=first)
+    E, T = len(counts), offsets[-1] + tail
+    a, sa, b, sb, c = operands(T, N, K, seed, True, experts=E)
+    b, sb, c = b.unflatten(0, (E, N)), sb.view(E, N), c.view(E, N)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    whole = torch.full((T + 2, (N + 7) // 8 * 8 + 8), 3.0, dtype=dtype, device="cuda")
+    d, other = whole[1:T + 1, :N], torch.full((T, (N + 7) // 8 * 8), 3.0, dtype=dtype, device="cuda")[:, :N]
+    fp4.fp4_selftest_gemm_int8(kernel, tile, split, a, sa, b, sb, d, off, c)
+    fp4.fp4_gemm_int8_grouped(a, sa, b, sb, off, other, c)
+    assert torch.equal(d, other), "other bits than the form that is chosen"
+    for e in range(E):
+        lo, hi = offsets[e:e + 2]
+        if lo < hi:
+            check_product(d[lo:hi], a[lo:hi], sa[lo:hi], b[e], sb[e], c[e], (form, e, lo, hi))
+            d[lo:hi] = 3.0
+    assert (whole == 3.0).all(), "wrote outside the groups"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("form", PAIR, ids=str)
+def test_pair_form_by_expert(form, dtype):
+    bt, pairs = form[1], cta_pairs()
+    grouped_by_form(form, [bt - 1, 0, bt, bt + 1, 1, 33, 0, 2 * bt + 31], 520, 330, dtype, bt, first=3, tail=40)
+    # eight token tiles of a wave and a bit: the last ones as halves, some of them narrow
+    grouped_by_form(form, [3 * bt - 31, 40, 3 * bt + 1], (pairs // 8 + 1) * 256 - 20, 300, dtype, bt + 1)
+    grouped_by_form(form, [7] * 70 + [0] * 20 + [bt // 2 + 1] * 9, 264, 1700, dtype, bt + 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("form", FEW, ids=str)
+def test_few_token_form_by_expert(form, dtype):
+    nt, split = form[1:]
+    grouped_by_form(form, [nt - 1, 0, nt, nt + 1, 1, 3, 0, 2 * nt + 5], 520, 1300, dtype, nt + split, first=3, tail=40)
+    grouped_by_form(form, [3] * 50 + [0] * 20 + [nt // 2 + 1] * 9 + [0], 1300, 1034, dtype, nt + split + 1)
