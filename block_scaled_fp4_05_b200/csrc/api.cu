@@ -689,6 +689,15 @@ fp4_status fp4_selftest_bounded_wait(fp4_stream_t stream)
     return from_cuda(fp4::launch_wait_selftest(reinterpret_cast<cudaStream_t>(stream)));
 }
 
+fp4_status fp4_selftest_bounded_wait_int8(fp4_stream_t stream)
+{
+    fp4::g_last_error[0] = 0;
+    fp4::DeviceInfo dev;
+    fp4_status st = require_device(&dev);
+    if (st != FP4_OK) return st;
+    return from_cuda(fp4::launch_int8_wait_selftest(reinterpret_cast<cudaStream_t>(stream)));
+}
+
 fp4_status fp4_get_device_status(fp4_stream_t stream)
 {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));

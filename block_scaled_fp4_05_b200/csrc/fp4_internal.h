@@ -128,6 +128,7 @@ cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const Int8Form* 
 // gemv_int8.cu: a few tokens and small weights
 bool gemv_int8_applies(const Int8GemmArgs& a);
 cudaError_t launch_gemv_int8(const Int8GemmArgs& a, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_int8_wait_selftest(cudaStream_t s);
 cudaError_t read_and_clear_int8_error_word(unsigned int* word);
 
 // Records the detail of a failure for fp4_last_error() (thread-local).

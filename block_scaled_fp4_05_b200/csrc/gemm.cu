@@ -1328,21 +1328,6 @@ fp4_gemm_pair_kernel(const __grid_constant__ PairArgs<NG> args)
     }
 }
 
-// Self-test of the bounded wait used by every kernel above: one thread waits
-// on a barrier that nothing will ever complete.  The wait gives up after
-// kTimeoutNs, records the error word, and the kernel returns normally.
-__global__ void bounded_wait_selftest_kernel()
-{
-    __shared__ __align__(8) uint64_t bar;
-    __shared__ int abort_flag;
-    if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&bar), 1);
-        abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        wait_bounded(smem_u32(&bar), 0, reinterpret_cast<volatile int*>(&abort_flag), ERR_SELFTEST);
-    }
-}
-
 // ------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------

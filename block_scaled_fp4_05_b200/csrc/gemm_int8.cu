@@ -1289,6 +1289,12 @@ cudaError_t launch_gemm_int8(const Int8GemmArgs& a, int kernel, const Int8Form* 
     return launch_pair_t(a, f.tile, most_token_tiles(a, f.tile) * ((a.N + 255) / 256), dev.sm_count, s);
 }
 
+cudaError_t launch_int8_wait_selftest(cudaStream_t s)
+{
+    bounded_wait_selftest_kernel<<<1, 32, 0, s>>>();
+    return cudaGetLastError();
+}
+
 cudaError_t read_and_clear_int8_error_word(unsigned int* word)
 {
     cudaError_t e = cudaMemcpyFromSymbol(word, g_fp4_error_word, sizeof(unsigned int));

@@ -383,6 +383,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return warp_wait_slow(bar, parity, abort_flag, code);
 }
 
+// Self-test of the bounded wait used by every tensor-core kernel: one thread waits
+// on a barrier that nothing will ever complete.  The wait gives up after
+// kTimeoutNs, records its unit's error word, and the kernel returns normally.
+__global__ void bounded_wait_selftest_kernel()
+{
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar), 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        wait_bounded(smem_u32(&bar), 0, reinterpret_cast<volatile int*>(&abort_flag), ERR_SELFTEST);
+    }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {

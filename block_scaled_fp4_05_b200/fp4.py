@@ -89,6 +89,8 @@ def lib():
         L.fp4_get_device_status.argtypes = [st]
         L.fp4_selftest_bounded_wait.restype = c.c_int
         L.fp4_selftest_bounded_wait.argtypes = [st]
+        L.fp4_selftest_bounded_wait_int8.restype = c.c_int
+        L.fp4_selftest_bounded_wait_int8.argtypes = [st]
         L.fp4_gemm_decode_dynamic.restype = c.c_int
         L.fp4_gemm_decode_dynamic.argtypes = [P, i64, P, P, P, i64, i64, i64, P, i64, P, P, P, sz, st]
         L.fp4_gemm_decode_noalloc.restype = c.c_int
@@ -469,6 +471,10 @@ def fp4_get_device_status(stream=None):
 
 def fp4_selftest_bounded_wait(stream=None):
     _check(lib().fp4_selftest_bounded_wait(_stream(stream)), "fp4_selftest_bounded_wait")
+
+
+def fp4_selftest_bounded_wait_int8(stream=None):
+    _check(lib().fp4_selftest_bounded_wait_int8(_stream(stream)), "fp4_selftest_bounded_wait_int8")
 
 
 def fp4_selftest_gemm_int8(kernel, tile, split, A, sA, B, sB, D, offsets=None, bias=None, stream=None):

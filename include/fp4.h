@@ -518,6 +518,10 @@ fp4_status fp4_get_device_status(fp4_stream_t stream);
  */
 fp4_status fp4_selftest_bounded_wait(fp4_stream_t stream);
 
+/* The same for the INT8 products, whose kernels record in an error word of
+ * their own (fp4_get_device_status reports and clears both). */
+fp4_status fp4_selftest_bounded_wait_int8(fp4_stream_t stream);
+
 /*
  * Self-test of the INT8 products: fp4_gemm_int8 (offsets NULL, E == 1) or
  * fp4_gemm_int8_grouped by a named form instead of the one that the library

@@ -850,3 +850,18 @@ def test_few_token_form_by_expert(form, dtype):
     nt, split = form[1:]
     grouped_by_form(form, [nt - 1, 0, nt, nt + 1, 1, 3, 0, 2 * nt + 5], 520, 1300, dtype, nt + split, first=3, tail=40)
     grouped_by_form(form, [3] * 50 + [0] * 20 + [nt // 2 + 1] * 9 + [0], 1300, 1034, dtype, nt + split + 1)
+
+
+# ---------------------------------------------------------------------------
+# A wait that gives up
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("both", [False, True])
+def test_a_timeout_of_an_int8_kernel_is_reported_and_cleared(both):
+    assert fp4.fp4_get_device_status() == 0
+    fp4.fp4_selftest_bounded_wait_int8()
+    if both:
+        fp4.fp4_selftest_bounded_wait()
+    assert fp4.fp4_get_device_status() == 5          # FP4_ERR_TIMEOUT, then cleared
+    assert fp4.fp4_get_device_status() == 0
+    a, sa, b, sb, bias = operands(300, 520, 640, 70, True)
+    check_product(fp4.gemm_int8(a, sa, b, sb, bias), a, sa, b, sb, bias)   # the context is usable
