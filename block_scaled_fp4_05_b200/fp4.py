@@ -18,7 +18,7 @@ GEMM_AUTO, GEMM_PREFILL, GEMM_DECODE = 0, 1, 2
 BF16, FP16 = 0, 1   # fp4_dtype: 16-bit types of the INT8 entry points
 GEMM_B_STATIC = 0x100   # flag: B / sB not written by a kernel still running on the stream
 
-FP4_OK = 0
+FP4_OK, FP4_ERR_MISALIGNED = 0, 3
 STATUS_NAMES = {
     0: "FP4_OK", 1: "FP4_ERR_INVALID_ARG", 2: "FP4_ERR_UNSUPPORTED_SHAPE",
     3: "FP4_ERR_MISALIGNED", 4: "FP4_ERR_CUDA", 5: "FP4_ERR_TIMEOUT", 6: "FP4_ERR_NO_DEVICE",
@@ -406,15 +406,23 @@ def _refuse_gemm(A, sA, B, sB, D, bias, kernel, stream=None, offsets=None, exper
                + ([("offsets", offsets, torch.int32, (channels[0] + 1,))] if experts else []))
 
 
+def _i8_check(status, name):
+    if status == FP4_ERR_MISALIGNED:
+        raise Fp4Error(status, name + " (the rows of every matrix have to start at multiples of 16 bytes, as those of"
+                                      " quantize_int8 and gemm_int8 do)")
+    _check(status, name)
+
+
 def fp4_quantize_int8(x, codes, scales, row_index=None, stream=None):
     """Per-row INT8 quantization of x [R x C] (bf16 or fp16) into codes (int8)
     and scales (float32): scales = amax / 127, codes = 127 x / amax rounded to
-    nearest even.  With row_index (int32) output row r is x[row_index[r]]."""
+    nearest even.  With row_index (int32) output row r is x[row_index[r]].
+    Rows of x and codes have to start at multiples of 16 bytes."""
     st = (_calls or _int8_calls()).quantize(x, codes, scales, row_index, _i8_stream(stream))
     if st != FP4_OK:
         if st < 0:
             _refuse_quantize(x, codes, scales, row_index)
-        _check(st, "fp4_quantize_int8")
+        _i8_check(st, "fp4_quantize_int8")
 
 
 def bind_quantize_int8(x, codes, scales, row_index=None, stream=None):
@@ -433,7 +441,7 @@ def fp4_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
     if st != FP4_OK:
         if st < 0:
             _refuse_gemm(A, sA, B, sB, D, bias, kernel)
-        _check(st, "fp4_gemm_int8")
+        _i8_check(st, "fp4_gemm_int8")
 
 
 def bind_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
@@ -453,7 +461,7 @@ def fp4_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias=None, kernel=GEMM_AUTO,
     if st != FP4_OK:
         if st < 0:
             _refuse_gemm(A, sA, B, sB, D, bias, kernel, offsets=offsets, experts=True)
-        _check(st, "fp4_gemm_int8_grouped")
+        _i8_check(st, "fp4_gemm_int8_grouped")
 
 
 def bind_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias=None, kernel=GEMM_AUTO, stream=None):
@@ -535,12 +543,19 @@ def _on(stream):
 
 
 def quantize_int8(x, row_index=None, stream=None):
-    """Per-row INT8 quantization of a bf16 or fp16 matrix; returns (codes, scales)."""
+    """Per-row INT8 quantization of a bf16 or fp16 matrix; returns (codes, scales).
+    An x whose rows do not start at multiples of 16 bytes (a width that is no
+    multiple of 8, some views) is first copied to rows that do."""
     rows = x.shape[0] if row_index is None else row_index.shape[0]
     with _on(stream):
         codes = _padded(rows, x.shape[1], 16, torch.int8, x.device)
         scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        fp4_quantize_int8(x, codes, scales, row_index)
+        try:
+            fp4_quantize_int8(x, codes, scales, row_index)
+        except Fp4Error as e:
+            if e.status != FP4_ERR_MISALIGNED:
+                raise
+            fp4_quantize_int8(_padded(*x.shape, 8, x.dtype, x.device).copy_(x), codes, scales, row_index)
     return codes, scales
 
 
@@ -564,8 +579,9 @@ def gemm_int8_grouped(A, sA, B, sB, offsets, bias=None, out=None, out_dtype=torc
 
 def linear_int8(x, W, sW, bias=None, out=None, stream=None):
     """x W^T + bias for a bf16 or fp16 activation x and a weight quantized ahead
-    of time by quantize_int8: the activation is quantized by token, then
-    multiplied; the result has x's type unless `out` is given.  The product
+    of time by quantize_int8: the activation is quantized by token (by
+    quantize_int8, so of any width), then multiplied; the result has x's type
+    unless `out` is given.  The product
     starts loading the weight while the activation's quantizer still runs; the
     weight's own may be the call right before."""
     with _on(stream):

@@ -865,3 +865,65 @@ def test_a_timeout_of_an_int8_kernel_is_reported_and_cleared(both):
     assert fp4.fp4_get_device_status() == 0
     a, sa, b, sb, bias = operands(300, 520, 640, 70, True)
     check_product(fp4.gemm_int8(a, sa, b, sb, bias), a, sa, b, sb, bias)   # the context is usable
+
+
+# ---------------------------------------------------------------------------
+# Tensors as they come: widths and views whose rows are not aligned
+# ---------------------------------------------------------------------------
+def as_they_come(g, dtype):
+    yield from (torch.randn(r, c, generator=g).to(dtype).cuda() for r, c in
+                [(5, 1), (3, 7), (1, 61), (40, 1001), (2, 4099), (3, 33001), (2, 12)])
+    x = torch.randn(9, 640, generator=g).to(dtype).cuda()
+    yield from (x[:, 1:], x[:, 3:500], x[1:, 4:12], x[::2, 7:8])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_quantize_tensors_as_they_come(dtype):
+    g = torch.Generator().manual_seed(71)
+    side = torch.cuda.Stream()
+    for x in as_they_come(g, dtype):
+        check_quantized(x, *fp4.quantize_int8(x), what=tuple(x.shape))
+        index = torch.randint(0, len(x), (13,), generator=g, dtype=torch.int32).cuda()
+        codes, scales = fp4.quantize_int8(x, index)
+        check_quantized(x[index.long()], codes, scales, tuple(x.shape))
+        torch.cuda.synchronize()
+        codes, scales = fp4.quantize_int8(x, stream=side)
+        side.synchronize()
+        check_quantized(x, codes, scales, tuple(x.shape))
+    for x in (torch.empty(0, 7, dtype=dtype, device="cuda"), torch.empty(3, 0, dtype=dtype, device="cuda")):
+        codes, scales = fp4.quantize_int8(x)
+        assert codes.shape == x.shape and (scales == 1).all()
+
+
+def test_linear_of_an_odd_width_and_its_graph():
+    g = torch.Generator().manual_seed(72)
+    N, K = 391, 1003
+    w, bias = (torch.randn(N, K, generator=g) * 0.02).to(BF).cuda(), torch.randn(N, generator=g).cuda()
+    W, sW = fp4.quantize_int8(w)
+    check_quantized(w, W, sW)
+    for M in (1, 9, 130):
+        x = torch.randn(M, K, generator=g).to(BF).cuda()
+        fp4.linear_int8(x, W, sW, bias)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = fp4.linear_int8(x, W, sW, bias)
+        for _ in range(2):
+            x.copy_(torch.randn(M, K, generator=g).to(BF))
+            graph.replay()
+            codes, scales = fp4.quantize_int8(x)
+            check_product(y, codes, scales, W, sW, bias)
+
+
+def test_calls_into_given_memory_say_what_is_misaligned():
+    x = torch.zeros(4, 61, dtype=BF, device="cuda")
+    codes, scales = torch.zeros(4, 64, dtype=torch.int8, device="cuda")[:, :61], torch.zeros(4, device="cuda")
+    for call in (lambda: fp4.fp4_quantize_int8(x, codes, scales),
+                 lambda: fp4.gemm_int8(codes.contiguous(), scales, codes, scales),
+                 lambda: fp4.gemm_int8_grouped(codes.contiguous(), scales, codes[None], scales[None],
+                                               torch.tensor([0, 4], dtype=torch.int32, device="cuda"))):
+        with pytest.raises(fp4.Fp4Error, match="multiples of 16 bytes") as e:
+            call()
+        assert e.value.status == 3
+    with pytest.raises(fp4.Fp4Error):                # no other error is taken for that one
+        fp4.quantize_int8(torch.zeros(1, 64, dtype=BF, device="cuda").expand(4, 64))
