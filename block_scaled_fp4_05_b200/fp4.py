@@ -436,7 +436,10 @@ def bind_quantize_int8(x, codes, scales, row_index=None, stream=None):
 
 def fp4_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
     """D [M x N] (bf16 or fp16) = (A @ B^T) * sA[:, None] * sB + bias for int8
-    A [M x K] and B [N x K]: exact integer sums, scaled and rounded once."""
+    A [M x K] and B [N x K]: exact integer sums, scaled in FP32 (sA first) and
+    rounded once.  With kernel | GEMM_B_STATIC the first weights are requested
+    while the kernel before, which may not be the one that writes them, still
+    runs."""
     st = (_calls or _int8_calls()).gemm(A, sA, B, sB, D, bias, kernel, _i8_stream(stream))
     if st != FP4_OK:
         if st < 0:

@@ -448,7 +448,10 @@ fp4_status fp4_quantize_int8(const void* in, fp4_dtype in_dtype, int64_t rows_in
  * D[m, n] = (sum_k A[m, k] B[n, k]) * sA[m] * sB[n] + bias[n]
  * for signed 8-bit A and B: the sum is exact (32-bit integers on the tensor
  * cores), the scales and the bias are applied in FP32 (the token's scale
- * first), and the result is rounded once to out_dtype.
+ * first), and the result is rounded once to out_dtype.  FP32's range holds on
+ * the way: where |sum| * sA is 2^128 or more (BF16 activations of about 1e32
+ * and above) the result is infinite, even if sB would bring it back; where it
+ * is below 2^-126, bits are lost as FP32's subnormals lose them.
  *   A : device, [M x K] bytes, leading dimension lda;  sA : M floats
  *   B : device, [N x K] bytes, leading dimension ldb;  sB : N floats
  *   bias : device, N floats, or NULL for none

@@ -927,3 +927,32 @@ def test_calls_into_given_memory_say_what_is_misaligned():
         assert e.value.status == 3
     with pytest.raises(fp4.Fp4Error):                # no other error is taken for that one
         fp4.quantize_int8(torch.zeros(1, 64, dtype=BF, device="cuda").expand(4, 64))
+
+
+# ---------------------------------------------------------------------------
+# FP32's range between the scales
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("M,N,K", [(4, 40, 200), (40, 136, 200), (300, 264, 200)])
+def test_products_of_huge_and_tiny_tokens(M, N, K):
+    # 127^2 K = 3225800 = 2^21.62: times 2^106 it fits FP32, times 2^107 it does not
+    a, b = torch.full((M, K + 8), 127, dtype=torch.int8, device="cuda")[:, :K], torch.full((N, K + 8), 127, dtype=torch.int8,
+                                                                                         device="cuda")[:, :K]
+    sums = 127.0 * 127 * K
+    sa, sb = torch.full((M,), 2.0 ** 106, device="cuda"), torch.full((N,), 2.0 ** -100, device="cuda")
+    sa[1::4], sa[2::4], sa[3::4] = 2.0 ** 107, 2.0 ** -126, 2.0 ** -149    # (2^-149: the smallest there is)
+    sb[1::2] = 2.0 ** 100
+    seen = []
+    for kernel in KERNELS:
+        d = fp4.gemm_int8(a, sa, b, sb, kernel=kernel).double()
+        # exact in FP32 where they fit: only the output's rounding, or its range
+        fits = (sums * sa.double()) < 2.0 ** 128
+        want = sums * sa.double()[:, None] * sb.double()[None, :]
+        assert torch.isinf(d[~fits]).all() and (d[~fits] > 0).all()
+        inside = fits[:, None] & (want < 3.3895e38) & (want >= 2.0 ** -126)
+        off = (d - want).abs()
+        assert (off[inside] <= 2.0 ** -8 * want[inside]).all()
+        small = fits[:, None] & (want < 2.0 ** -126)
+        assert (off[small] <= 2.0 ** -134 + 2.0 ** -150).all()             # half a step of BF16's subnormals, and of FP32's
+        assert torch.isinf(d[fits[:, None] & (want > 3.4e38)]).all()
+        seen.append(d)
+    assert all(torch.equal(d, seen[0]) for d in seen)
