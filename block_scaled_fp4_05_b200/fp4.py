@@ -459,7 +459,8 @@ def bind_gemm_int8(A, sA, B, sB, D, bias=None, kernel=GEMM_AUTO, stream=None):
 def fp4_gemm_int8_grouped(A, sA, B, sB, offsets, D, bias=None, kernel=GEMM_AUTO, stream=None):
     """fp4_gemm_int8 by expert: rows offsets[e] .. offsets[e + 1] of A and D
     with B[e] [N x K], sB[e] and bias[e].  offsets (int32, E + 1) is read on
-    the device; rows of D in no group are left as they were."""
+    the device; rows of D in no group are left as they were.  GEMM_B_STATIC is
+    taken and changes nothing here."""
     st = (_calls or _int8_calls()).grouped(A, sA, B, sB, offsets, D, bias, kernel, _i8_stream(stream))
     if st != FP4_OK:
         if st < 0:

@@ -489,6 +489,8 @@ fp4_status fp4_gemm_int8(const void* A, int64_t lda, const float* sA, const void
  *   E : 0 <= E <= 512;  T : rows of A, sA and D
  * Rows of D before offsets[0] and from offsets[E] on are left as they were;
  * experts without rows cost nothing.  FP4_GEMM_AUTO estimates from T / E.
+ * FP4_GEMM_B_STATIC is taken and changes nothing: which experts' weights are
+ * needed is not known before the offsets are read.
  * Requires stride_b % 16 == 0 and stride_b >= (N - 1) * ldb + K, else as
  * fp4_gemm_int8.
  */
