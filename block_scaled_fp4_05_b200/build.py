@@ -10,7 +10,9 @@ library loads on machines without a GPU.
 
 The Python calls of the INT8 entry points (csrc/int8_calls.cpp) are a small
 extension module beside it, _int8_calls.so, compiled by g++ against torch's
-headers: host code alone, which takes its entry points from libfp4.so.
+headers: host code alone, which takes its entry points from libfp4.so.  It
+holds what it was built for (torch's version, Python's ABI) and is built anew
+when that changes.
 """
 import os
 import shutil
@@ -56,9 +58,27 @@ def _newer(out, inputs):
     return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in inputs)
 
 
+def calls_target():
+    """What _int8_calls.so has to be built for: the layouts of torch's tensors
+    and of Python's objects are compiled into it."""
+    import torch
+
+    return "torch %s, %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
+def lib_up_to_date():
+    return _newer(LIB, _inputs())
+
+
+def calls_up_to_date():
+    if not _newer(CALLS, [CALLS_SOURCE, os.path.join(INCLUDE, "fp4.h")]):
+        return False
+    with open(CALLS, "rb") as f:
+        return calls_target().encode() + b"\0" in f.read()
+
+
 def up_to_date():
-    return (_newer(LIB, _inputs())
-            and _newer(CALLS, [CALLS_SOURCE, os.path.join(INCLUDE, "fp4.h")]))
+    return lib_up_to_date() and calls_up_to_date()
 
 
 def build_calls(verbose=False):
@@ -70,6 +90,7 @@ def build_calls(verbose=False):
     tmp = CALLS + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wno-attributes",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           '-DFP4_BUILT_FOR="%s"' % calls_target(),
            "-I", os.path.join(home, "include"),
            "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
            "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
@@ -84,9 +105,7 @@ def build_calls(verbose=False):
     return CALLS
 
 
-def build(force=False, verbose=False):
-    if not force and up_to_date():
-        return LIB
+def build_lib(verbose=False):
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
     if verbose:
@@ -98,7 +117,14 @@ def build(force=False, verbose=False):
     if verbose:
         sys.stderr.write(r.stdout + r.stderr)
     os.replace(tmp, LIB)
-    build_calls(verbose)
+    return LIB
+
+
+def build(force=False, verbose=False):
+    if force or not lib_up_to_date():
+        build_lib(verbose)
+    if force or not calls_up_to_date():
+        build_calls(verbose)
     return LIB
 
 

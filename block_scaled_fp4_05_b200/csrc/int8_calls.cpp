@@ -8,6 +8,7 @@
 // status, or -1 without a call where a tensor does not fit (the caller finds
 // out which); the *_args functions return the C arguments as a tuple, or None.
 // stream is None for the current stream, else a handle as an integer.
+// built_for names the torch and the Python whose headers it was compiled with.
 
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -266,4 +267,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_int8_calls", nullptr, -1, g_met
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__int8_calls(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__int8_calls(void)
+{
+    PyObject* m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", FP4_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -345,15 +345,21 @@ _calls = None
 
 def _int8_calls():
     """The extension module that checks and marshals these calls (raises if it
-    has not been built)."""
+    has not been built, or for another torch or Python)."""
     global _calls
     if _calls is None:
+        from .build import calls_target
+
         L = lib()
         try:
             from . import _int8_calls as m
         except ImportError as e:
-            raise RuntimeError("_int8_calls.so is missing; build it with "
-                               "`python -m block_scaled_fp4_05_b200.build`") from e
+            raise RuntimeError("_int8_calls.so cannot be loaded (%s); build it with "
+                               "`python -m block_scaled_fp4_05_b200.build`" % e) from e
+        target = calls_target()
+        if m.built_for != target:
+            raise RuntimeError("_int8_calls.so was built for %s, this is %s; build it with "
+                               "`python -m block_scaled_fp4_05_b200.build`" % (m.built_for, target))
         m.set_entry_points(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                              (L.fp4_quantize_int8, L.fp4_gemm_int8, L.fp4_gemm_int8_grouped)))
         _calls = m
