@@ -21,6 +21,7 @@ import datetime
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -109,10 +110,21 @@ class ClockSampler:
                 "reasons": sorted(reasons)}
 
 
-def kernel_source_hash():
+def kernel_sources(csrc):
+    """The files of `csrc` that the timed kernels are compiled from: their two
+    sources and, from file to file, the headers beside them."""
+    files = ["gemm.cu", "quantize.cu"]
+    for f in files:
+        with open(os.path.join(csrc, f)) as fh:
+            found = re.findall(r'^\s*#\s*include\s+"([^"/]+)"', fh.read(), re.M)
+        files += [h for h in found if h not in files and os.path.exists(os.path.join(csrc, h))]
+    return files
+
+
+def kernel_source_hash(csrc=os.path.join(ROOT, "block_scaled_fp4_05_b200", "csrc")):
     h = hashlib.sha256()
-    for f in ("gemm.cu", "quantize.cu"):
-        with open(os.path.join(ROOT, "block_scaled_fp4_05_b200", "csrc", f), "rb") as fh:
+    for f in sorted(kernel_sources(csrc)):
+        with open(os.path.join(csrc, f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
 

@@ -1,6 +1,8 @@
 """What is built anew when: the library by its sources, the extension module of
-the INT8 calls also by the torch and the Python that it was compiled for."""
+the INT8 calls also by the torch and the Python that it was compiled for.  And
+which sources the recorded DRAM traffic of the FP4 kernels hangs on."""
 import os
+import shutil
 import sys
 
 import pytest
@@ -62,3 +64,22 @@ def test_why_a_module_does_not_load_is_said(monkeypatch):
     monkeypatch.setitem(sys.modules, name, None)
     with pytest.raises(RuntimeError, match="cannot be loaded .*%s" % os.path.basename(name)):
         fp4._int8_calls()
+
+
+def test_recorded_traffic_hangs_on_the_headers_too(tmp_path):
+    import bench
+    sources = bench.kernel_sources(build.CSRC)
+    assert {"gemm.cu", "quantize.cu", "tc_device.cuh", "quant_device.cuh", "fp4_internal.h"} <= set(sources)
+    for name in sources:
+        copy = str(tmp_path / name)
+        shutil.copytree(build.CSRC, copy)
+        assert bench.kernel_source_hash(copy) == bench.kernel_source_hash()
+        with open(os.path.join(copy, name), "a") as f:
+            f.write("// another byte\n")
+        assert bench.kernel_source_hash(copy) != bench.kernel_source_hash()
+    with open(os.path.join(copy, "gemm_int8.cu"), "a") as f:   # no part of these kernels
+        f.write("\n")
+    with open(os.path.join(copy, name), "rb+") as f:
+        f.seek(-len("// another byte\n"), 2)
+        f.truncate()
+    assert bench.kernel_source_hash(copy) == bench.kernel_source_hash()
