@@ -99,6 +99,10 @@ cudaError_t launch_quantize_int8(int dtype, const uint16_t* x, int64_t rows_in, 
                                  const int32_t* row_index, int64_t rows, int8_t* codes, int64_t ldc,
                                  float* scales, cudaStream_t s);
 
+// The pair GEMM of gemm.cu: a cluster whose CTAs hold all tensor memory of
+// their SMs and at least this much shared memory.
+constexpr int kFp4PairSmem = 197120;
+
 // gemm_int8.cu
 constexpr int kInt8MaxExperts = 512;   // the pair kernel keeps the experts' tile list in shared memory
 struct Int8GemmArgs {

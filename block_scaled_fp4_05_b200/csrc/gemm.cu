@@ -1548,6 +1548,8 @@ cudaError_t launch_pair_kernel(const PairArgs<NG>& args, int grid, cudaStream_t 
 
 constexpr int PAIR_STAGES_NV = 5;   // 38 KB per stage
 constexpr int PAIR_STAGES_MX = 5;   // 35 KB per stage
+static_assert(PairCfg<PAIR_STAGES_NV, false>::SMEM >= kFp4PairSmem && PairCfg<PAIR_STAGES_MX, true>::SMEM >= kFp4PairSmem,
+              "what gemm_int8.cu counts on");
 
 // Fills problem slot g of a pair-kernel launch (tensor maps and Params).
 template <int NG>

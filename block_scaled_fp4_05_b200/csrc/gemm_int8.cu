@@ -1049,11 +1049,21 @@ int swap_ctas(int nt, int split, double clusters, const Held& held)
 
 // Stages of the few-token kernel: those of a CTA's share of K, as far as they
 // fit beside the other CTAs of the SM.
-constexpr int swap_stages(int nt, int ctas, int share)
+//
+// A cluster asks for two at least, so that its CTAs never share an SM with
+// those of the FP4 pair GEMM on another stream.  Both wait for tensor memory
+// without a limit, and both wait for the rest of their cluster: with a CTA of
+// each on two SMs, one ahead on either, none of the four would ever go on.
+// (One stage: 21.5 KB, which fit beside the pair GEMM of MXFP4.  A CTA that is
+// no cluster's waits for nothing but the tensor memory.)
+constexpr int kClusterStages = 2;
+static_assert(SwapCfg<16>::smem(kClusterStages) + 1024 + kFp4PairSmem + 1024 > kSmSmem, "no room for both on an SM");
+constexpr int swap_stages(int nt, int split, int ctas, int share)
 {
     const int bytes = I8_TILE + nt * I8_BK, fixed = 1024 + SwapCfg<128>::FIXED;
     const int room = (kSmSmem / ctas - 1024 - fixed) / bytes;
-    const int least = (nt * I8_BM * 4 + bytes - 1) / bytes;   // the sums take their memory
+    const int sums = (nt * I8_BM * 4 + bytes - 1) / bytes;   // the sums take their memory
+    const int least = split > 1 && sums < kClusterStages ? kClusterStages : sums;
     const int n = share < room ? share : room;
     return n < least ? least : n > SwapCfg<128>::MAX_STAGES ? SwapCfg<128>::MAX_STAGES : n;
 }
@@ -1079,7 +1089,7 @@ cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, cons
         const int64_t hold = held.of(split, swap_resident(NT));
         const unsigned grid = (unsigned)((clusters < hold ? clusters : hold) * split);
         I8Params p = params_of(a, I8_BM);
-        p.stages = swap_stages(NT, swap_ctas(NT, split, (double)clusters, held), (p.ks_total + split - 1) / split);
+        p.stages = swap_stages(NT, split, swap_ctas(NT, split, (double)clusters, held), (p.ks_total + split - 1) / split);
         launch_config(cfg, attr, grid, kSwapThreads, (unsigned)split, C::smem(p.stages), s);
         e = cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
     }

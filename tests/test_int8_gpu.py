@@ -956,3 +956,31 @@ def test_products_of_huge_and_tiny_tokens(M, N, K):
         assert torch.isinf(d[fits[:, None] & (want > 3.4e38)]).all()
         seen.append(d)
     assert all(torch.equal(d, seen[0]) for d in seen)
+
+
+# ---------------------------------------------------------------------------
+# Beside the FP4 GEMM
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", [fp4.NVFP4, fp4.MXFP4])
+@pytest.mark.parametrize("split", [2, 8])
+def test_clusters_beside_the_fp4_pair_gemm_on_another_stream(fmt, split):
+    # clusters of one stage's work each, and CTA pairs that take all tensor memory
+    g = torch.Generator().manual_seed(73)
+    M, N, K = 20, 1000, 128 * split - 24
+    a, sa, b, sb, bias = operands(M, N, K, 74, True)
+    d = torch.zeros(M, 1000, dtype=BF, device="cuda")
+    R, KF = 512, 1024
+    codes = [torch.randint(0, 256, (R, KF // 2), generator=g, dtype=torch.uint8).cuda() for _ in range(2)]
+    one = 127 if fmt == fp4.MXFP4 else 0x38                   # 1.0 in E8M0 and in E4M3
+    scales = [torch.full((fp4.fp4_scale_bytes(fmt, R, KF),), one, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    alpha = torch.ones(1, device="cuda") if fmt == fp4.NVFP4 else None
+    outs = [torch.zeros(R, R, dtype=BF, device="cuda") for _ in range(2)]
+    fp4.gemm(fmt, codes[0], scales[0], codes[1], scales[1], KF, alpha, fp4.GEMM_PREFILL, outs[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(200):
+        fp4.gemm(fmt, codes[0], scales[0], codes[1], scales[1], KF, alpha, fp4.GEMM_PREFILL, outs[1], stream=streams[0])
+        fp4.fp4_selftest_gemm_int8(fp4.GEMM_DECODE, 16, split, a, sa, b, sb, d, bias=bias, stream=streams[1])
+    torch.cuda.synchronize()
+    check_product(d, a, sa, b, sb, bias)
+    assert torch.equal(outs[0], outs[1])
