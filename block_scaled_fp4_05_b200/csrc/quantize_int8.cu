@@ -21,10 +21,16 @@
 // once; rows above 32768 elements are read twice (the second time mostly from
 // L2).  Short-lived blocks, one row each (a warp a row up to 2048 elements),
 // keep more loads in flight than blocks that load a row ahead while they work
-// on one (8194 rows of 4096: 18.9, two rows a block 19.5, eight 21.7 us).
-// Measured on a B200, of 6559 GB/s: 8192x8192 31.1 us (99 %), 8194x4096 16.3
-// us (94 %); 8194 rows gathered from 4097 of 4096 16.6 us, where latency and
-// instructions bind (59 % of the issue slots), not HBM.
+// on one (8194 rows of 4096, an earlier state of this kernel: two rows a block
+// 3 % slower, eight 15 %).
+// Measured on a B200 at 1965 MHz, launches of a graph over inputs larger than
+// L2, of 6559 GB/s: 8192x8192 31.0 us (99 %), 8194x4096 16.3 (94 %),
+// 16384x2048 16.4 (93 %); widths that leave some threads' last chunk empty
+// 8192x7168 28.2 (95 %), 8192x5120 21.3 (90 %), 4096x28672 61.2 (88 %),
+// 8192x2880 13.8 (78 %).  Gathered rows are read, searched and converted once
+// a copy: 2 copies of 4097 rows of 4096 16.0 us of 10.2 for the bytes, 8 of
+// 4096 rows 53.2 of 25.6, where latency and instructions bind (53 % of the
+// issue slots), not HBM.
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -278,19 +284,19 @@ cudaError_t launch(const QuantArgs& p, cudaStream_t s)
 template <bool HALF>
 cudaError_t dispatch(const QuantArgs& p, cudaStream_t s)
 {
-    // A warp a row while it holds it: 16384 rows of 2048 18.4 us, 19.8 with a
+    // A warp a row while it holds it: 16384 rows of 2048 16.5 us, 18.1 with a
     // block of 128 threads a row.
     if (p.cols <= 256) return launch<HALF, 32, 1, 128>(p, s);
     if (p.cols <= 512) return launch<HALF, 32, 2, 128>(p, s);
     if (p.cols <= 1024) return launch<HALF, 32, 4, 128>(p, s);
     if (p.cols <= 2048) return launch<HALF, 32, 8, 128>(p, s);
     // Then a block a row.  Many rows: more chunks a thread, so that more bytes
-    // are in flight (8192 rows of 8192: 8 chunks 33.2, 4 33.9, 2 42.3 us; 8194
-    // of 4096: 4 17.8, 2 20.9).  Few: more threads (one row of 4096: 2 chunks
-    // 1.8, 4 2.1, 8 2.5 us; of 8192: 4 chunks 2.1, 8 2.6).  Gathered rows come
-    // from L2 in part, and then the reductions' instructions count: half as
-    // many threads (8194 rows of 4096 from 4097 17.0 -> 15.9 us, 4000 from 2000
-    // 7.0 -> 6.5; 2000 from 1000 4.1 -> 4.3; in order 16.3 -> 16.6).
+    // are in flight (8192 rows of 8192: 8 chunks 31.2, 4 30.9, 2 38.5 us; 8194
+    // of 4096: 4 16.4, 2 18.1).  Few: more threads (one row of 4096: 2 chunks
+    // 1.15, 4 1.23, 8 1.48 us; of 8192: 4 chunks 1.40, 8 1.49).  Gathered rows
+    // come from L2 in part, and then the reductions' instructions count: half
+    // as many threads (8194 rows of 4096 from 4097 17.1 -> 16.0 us, 4000 from
+    // 2000 9.4 -> 8.7; 2000 from 1000 5.7 -> 5.6; in order 16.4 -> 16.6).
     const bool many = p.rows > 1024;
     if (p.cols <= 4096 && p.index && p.rows > 3000) return launch<HALF, 64, 8, 64>(p, s);
     if (p.cols <= 4096) return many ? launch<HALF, 128, 4, 128>(p, s) : launch<HALF, 256, 2, 256>(p, s);
