@@ -1068,6 +1068,16 @@ constexpr int swap_stages(int nt, int split, int ctas, int share)
     return n < least ? least : n > SwapCfg<128>::MAX_STAGES ? SwapCfg<128>::MAX_STAGES : n;
 }
 
+// As many CTAs as an SM's shared memory holds, whatever their tiles, ask for no
+// more than its 512 columns of tensor memory.
+template <int NT>
+constexpr bool columns_suffice(int split)
+{
+    return (int64_t)SwapCfg<NT>::TMEM_COLS * kSmSmem <= 512ll * (SwapCfg<NT>::smem(swap_stages(NT, split, 3, 1)) + 1024);
+}
+static_assert(columns_suffice<16>(1) && columns_suffice<32>(1) && columns_suffice<64>(1) && columns_suffice<128>(1),
+              "tensor memory of the CTAs on an SM");
+
 template <int NT, bool HALF>
 cudaError_t launch_swap(const Int8GemmArgs& a, int split, int64_t clusters, const Held& held, cudaStream_t s)
 {
