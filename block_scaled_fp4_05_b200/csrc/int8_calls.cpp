@@ -150,7 +150,8 @@ struct Gemm {
         sB = static_cast<const float*>(sb->data_ptr());
         bias = c ? static_cast<const float*>(c->data_ptr()) : nullptr;
         offsets = o ? static_cast<const int32_t*>(o->data_ptr()) : nullptr;
-        kernel = (int)PyLong_AsLong(pkernel);
+        const long choice = PyLong_AsLong(pkernel);
+        kernel = choice == (int)choice ? (int)choice : -1;   // (which the call refuses)
         return !PyErr_Occurred() && stream_of(pstream, device, &stream);
     }
 };

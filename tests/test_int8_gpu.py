@@ -984,3 +984,13 @@ def test_clusters_beside_the_fp4_pair_gemm_on_another_stream(fmt, split):
     torch.cuda.synchronize()
     check_product(d, a, sa, b, sb, bias)
     assert torch.equal(outs[0], outs[1])
+
+
+def test_kernel_numbers_that_leave_32_bits_are_refused():
+    a, sa, b, sb, _ = operands(4, 16, 64, 75, False)
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    for kernel in (1 << 32, (1 << 32) | fp4.GEMM_DECODE, -(1 << 32), 1 << 70, -1):
+        with pytest.raises((ValueError, OverflowError, fp4.Fp4Error)):
+            fp4.gemm_int8(a, sa, b, sb, kernel=kernel)
+        with pytest.raises((ValueError, OverflowError, fp4.Fp4Error)):
+            fp4.gemm_int8_grouped(a, sa, b[None], sb[None], off, kernel=kernel)
